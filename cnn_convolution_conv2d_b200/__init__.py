@@ -90,10 +90,11 @@ def load():
                 f"{LIBRARY} is missing: build it with `python -m cnn_convolution_conv2d_b200.build` "
                 "(there is no fallback implementation)")
         lib = ctypes.CDLL(LIBRARY)
-        for name, (args, res) in SIGNATURES.items():
-            fn = getattr(lib, name)
-            fn.argtypes = args
-            fn.restype = res
+        for table in (SIGNATURES, sequence.SIGNATURES, optimizer.SIGNATURES):
+            for name, (args, res) in table.items():
+                fn = getattr(lib, name)
+                fn.argtypes = args
+                fn.restype = res
         _lib = lib
     return _lib
 
@@ -536,6 +537,13 @@ class Conv2dB200:
         self.bias = None if bias is None else bias.to(w.dtype).contiguous()
         self._ws = {}
 
+    def repack(self, stream=None):
+        """Packs the weight tensor the layer was made from again, after it was updated in place
+        (``AdamWB200``); the bias is read where it lies if it had the weight's dtype."""
+        conv2d_pack_weight(self._w_oihw, self.groups, self.w_packed, stream)
+        if self.w_packed_t is not None:
+            conv2d_pack_weight_backward_data(self._w_oihw, self.groups, self.w_packed_t, stream)
+
     def out_shape(self, N, H, W):
         Ho = conv2d_output_size(H, self.Kh, self.stride, self.pad, self.dilation)
         Wo = conv2d_output_size(W, self.Kw, self.stride, self.pad, self.dilation)
@@ -614,3 +622,12 @@ class Conv2dB200:
         return conv2d_forward_hostio(x_host, y_host, x_dev, y_dev, self.w_packed, self.bias,
                                      *self._shape_args(N, H, W), self.dtype, self.layout,
                                      self.workspace(N, H, W), stream)
+
+
+# Operators over sequences and the weight update (include/sequence_b200.h, include/optimizer_b200.h).
+from . import sequence  # noqa: E402
+from .sequence import (CONV_ACT_NONE, CONV_ACT_SILU, CausalConv1dB200, GatedRecurrenceB200,  # noqa: E402,F401
+                       conv1d_causal_backward_workspace_size, gated_recurrence_backward_workspace_size,
+                       gated_recurrence_saved_size, gated_recurrence_workspace_size)
+from . import optimizer  # noqa: E402
+from .optimizer import AdamWB200  # noqa: E402,F401

@@ -13,6 +13,7 @@
 
 #include "common.cuh"
 #include "conv2d_b200.h"
+#include "host.cuh"
 
 namespace conv2d_b200 {
 namespace {
@@ -1777,6 +1778,29 @@ int packed_weight_t_bytes(int C_out, int C_in, int Kh, int Kw, int groups, int e
     return 0;
 }
 }  // namespace
+
+// ------------------------------------------------ for the other entry files ---
+int abi_fail(int status, const char *fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    return fail(status, "%s", buf);
+}
+
+int abi_ok() { return ok(); }
+
+int abi_launch(cudaError_t e, const char *what) { return check_launch(e, what); }
+
+int abi_device(AbiDevice *out) {
+    DeviceInfo *dev = nullptr;
+    const int st = device_info(&dev);
+    if (st != CONV_OK) return st;
+    const Settings cfg = settings_now();
+    *out = AbiDevice{dev->sms, dev->status, cfg.timeout_ns, cfg.starve};
+    return CONV_OK;
+}
 }  // namespace conv2d_b200
 
 using namespace conv2d_b200;
@@ -2021,6 +2045,9 @@ int conv2d_sync_status(conv_stream_t stream) {
     if (v != 0) {
         const int zero = 0;
         cudaMemcpy(dev->status, &zero, sizeof(int), cudaMemcpyHostToDevice);
+        if (v == kDevBadOffsets)
+            return fail(CONV_ERR_INVALID_ARG, "sequence offsets must begin at 0, never fall and end inside the rows");
+        if (v == kDevBadSlot) return fail(CONV_ERR_INVALID_ARG, "two rows of a step named the same slot");
         return fail(CONV_ERR_TIMEOUT, "device watchdog fired (code %d)", v);
     }
     return ok();

@@ -1,0 +1,41 @@
+// adamw.cuh -- one launch of the AdamW kernel.
+#pragma once
+
+#include "common.cuh"
+
+namespace conv2d_b200 {
+
+constexpr int kAdamTensors = 48;     // tensors of one launch: their table travels as a kernel argument
+constexpr int kAdamThreads = 256;
+constexpr int kAdamPerThread = 8;
+constexpr int kAdamQuant = 256;      // elements of one scale of an 8-bit state: a warp's
+constexpr int kAdamPerBlock = kAdamThreads * kAdamPerThread;
+
+struct AdamTensor {
+    void *p;
+    float *master;
+    const void *g;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    long long n;
+};
+
+struct AdamParams {
+    AdamTensor t[kAdamTensors];
+    unsigned first[kAdamTensors + 1];  // the first block of each tensor; [count]: all blocks
+    int count;
+    unsigned index0;                   // the first tensor's place in the whole list
+    float beta1, beta1c, beta2, beta2c;  // c: 1 - beta
+    float keep;                        // 1 - lr * weight_decay
+    float rate, root;                  // lr / (1 - beta1^step), 1 / sqrt(1 - beta2^step)
+    float eps;
+    double lr, ln_beta1, ln_beta2;     // for a step read on the device
+    long long step;
+    const long long *step_device;
+    const float *grad_scale;
+    unsigned seed;
+};
+
+cudaError_t launch_adamw(const AdamParams &p, bool p32, bool g32, bool master, bool eight, cudaStream_t s);
+
+}  // namespace conv2d_b200

@@ -24,6 +24,9 @@ enum DeviceStatus : int {
     kDevTimeoutAccEmpty = 4, // the tensor-core warp waited too long for a free accumulator
     kDevTimeoutConvert = 5,  // fp32 split warps waited too long
     kDevBadCoordinate = 6,   // a load coordinate failed the 16-byte rule (load skipped)
+    kDevTimeoutCarry = 7,    // a chunk of a recurrence waited too long for the one before it
+    kDevBadOffsets = 8,      // sequence offsets fall, or leave the rows
+    kDevBadSlot = 9,         // two rows of a step name the same slot (the later one was skipped)
 };
 
 // Everything one launch of the implicit-GEMM kernel needs.  Rows of the

@@ -1,0 +1,170 @@
+// sequence.cuh -- what the kernels over sequences (conv1d.cu, recurrence.cu) share: the
+// description of the rows of a batch, element access, and the launchers' parameters.
+//
+// A tensor over sequences is a matrix of `rows` rows of C channels (channels-last, the last
+// dimension contiguous, rows a fixed stride apart).  Either the rows are nseq sequences of
+// T rows each, or `offsets` (nseq + 1 device ints) packs sequences of their own lengths one
+// behind the other: sequence s has rows offsets[s] .. offsets[s+1]-1.  Rows from
+// offsets[nseq] on belong to none; nothing is written there.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+
+namespace conv2d_b200 {
+
+struct Sequences {
+    const int *offsets;  // NULL: nseq sequences of T rows
+    int nseq;
+    int T;
+    int rows;
+};
+
+struct Conv1dParams {
+    const void *x, *w, *bias, *dy;
+    void *y;               // forward: y; backward: dx
+    const void *state;     // (nseq, K-1, C) rows before each sequence, or NULL (zeros)
+    void *final_state;     // forward: (nseq, K-1, C) or NULL
+    const void *d_final;   // backward: gradient of final_state, or NULL
+    void *d_state;         // backward: gradient of state, or NULL
+    float *partial;        // backward: [row blocks][K+1][C] sums of dw (taps 0..K-1) and db
+    long long ldx, ldy, lddy;  // row strides in elements: x, the output, dy
+    Sequences seq;
+    int C, K, silu;
+    int strip;             // rows of one warp
+    int tiles;             // channel tiles
+    int row_blocks;        // blocks of kConvWarps strips; blocks behind them copy states
+    int *status;
+};
+
+struct Conv1dStepParams {
+    const void *x, *w, *bias;
+    void *y, *state;
+    const int *slots;      // row b's window is state[slots[b]]; NULL: state[b]
+    long long ldx, ldy;
+    int B, C, K, silu, pool, tiles;
+    int *status;
+};
+
+struct RecParams {
+    const void *x, *ga, *gx, *dy;
+    const float *decay;    // (C,)
+    float kappa;
+    void *y;               // forward: h; backward: dx
+    void *dga, *dgx;       // backward
+    const float *state;    // (nseq, C) or NULL
+    float *final_state;    // forward: (nseq, C) or NULL
+    const float *d_final;  // backward: gradient of final_state, or NULL
+    float *d_state;        // backward: gradient of state, or NULL
+    float *decay_partial;  // backward: [chunks][Cpad] sums
+    const float *saved;    // backward: the forward pass's carries
+    float *carry;          // [chunks][Cpad] carries behind each chunk (forward: the saved states)
+    float2 *aggregate;     // [chunks][Cpad] (product of decays, state of a zero start)
+    unsigned *ticket;      // starts at 0xffffffff
+    long long ldx, lda, ldg, ldy, lddy, ld_da, ld_dg;
+    Sequences seq;
+    int C, Cpad, tiles, chunks;
+    int *status;
+    long long timeout_ns;
+    int starve;
+};
+
+struct RecStepParams {
+    const void *x, *ga, *gx;
+    const float *decay;
+    float kappa;
+    void *y;
+    float *state;
+    const int *slots;
+    long long ldx, lda, ldg, ldy;
+    int B, C, pool, tiles;
+    int *status;
+};
+
+constexpr int kConvWarps = 4;     // warps of a conv1d block, one strip of rows each
+constexpr int kRecChunk = 128;    // rows of one work item of the recurrence, and of one saved carry
+constexpr int kRecTile = 64;      // channels of one work item
+
+cudaError_t launch_conv1d_forward(const Conv1dParams &p, bool f32, bool vec, cudaStream_t s);
+cudaError_t launch_conv1d_backward(const Conv1dParams &p, bool f32, bool vec, cudaStream_t s);
+cudaError_t launch_conv1d_reduce(const float *partial, void *dw, void *db, int row_blocks, int C, int K, bool f32,
+                                 cudaStream_t s);
+cudaError_t launch_conv1d_step(const Conv1dStepParams &p, bool f32, bool vec, cudaStream_t s);
+int conv1d_strip(int rows, int C, int K, int sms);
+int conv1d_channels_per_block(int K);
+
+cudaError_t launch_rec_init(const RecParams &p, size_t words, float *carry, size_t carry_words, cudaStream_t s);
+cudaError_t launch_rec_forward(const RecParams &p, bool f32, bool vec, int sms, cudaStream_t s);
+cudaError_t launch_rec_backward(const RecParams &p, bool f32, bool vec, int sms, cudaStream_t s);
+cudaError_t launch_rec_decay(const float *partial, const float *decay, float kappa, float *d_decay, int chunks, int C,
+                             int Cpad, cudaStream_t s);
+cudaError_t launch_rec_step(const RecStepParams &p, bool f32, bool vec, cudaStream_t s);
+
+#ifdef __CUDACC__
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T from_float(float v);
+template <> __device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// First row of sequence s, kept inside [0, rows] whatever the offsets hold.
+__device__ __forceinline__ int seq_begin(const Sequences &q, int s) {
+    if (!q.offsets) return s * q.T;
+    return min(max(q.offsets[s], 0), q.rows);
+}
+
+// The last sequence that begins at or before `row` (-1: none): with empty sequences at that
+// row, the one that holds it.
+__device__ __forceinline__ int seq_of(const Sequences &q, int row) {
+    if (!q.offsets) return q.T > 0 ? min(row / q.T, q.nseq - 1) : -1;
+    int lo = -1, hi = q.nseq - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (q.offsets[mid] <= row) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Whether the offsets begin at 0, never fall and end inside the rows.  Called by all threads
+// of one block; a violation is reported through the status word.
+__device__ __forceinline__ void check_offsets(const Sequences &q, int *status) {
+    if (!q.offsets) return;
+    for (int s = threadIdx.x; s <= q.nseq; s += blockDim.x) {
+        const int v = q.offsets[s], before = s ? q.offsets[s - 1] : 0;
+        if (v < before || v > q.rows || (s == 0 && v != 0)) atomicExch(status, kDevBadOffsets);
+    }
+}
+
+// Whether an earlier row of the batch names the same slot.  Called by all threads of a block.
+__device__ __forceinline__ bool slot_named_before(const int *slots, int b, int slot) {
+    int dup = 0;
+    for (int j = threadIdx.x; j < b; j += blockDim.x) dup |= slots[j] == slot;
+    return __syncthreads_or(dup) != 0;
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rsqrt_approx(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 1 / (1 + e^-z).  Where e^-z passes the largest float, 1/inf = 0 is the right value.
+__device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.f + ex2_approx(z * -kLog2e)); }
+
+#endif  // __CUDACC__
+
+}  // namespace conv2d_b200

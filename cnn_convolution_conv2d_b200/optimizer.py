@@ -1,0 +1,129 @@
+"""AdamW over many tensors at once, a thin binding of ``include/optimizer_b200.h``.
+
+``AdamWB200`` owns the states of a list of weights (of any layers: a gradient has its
+weight's layout) and updates all of them in a few launches.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _check, _dtype_code, load
+from .sequence import _on
+
+_I, _P, _L, _D = ctypes.c_int, ctypes.c_void_p, ctypes.c_longlong, ctypes.c_double
+
+
+class AdamWTensor(ctypes.Structure):
+    """adamw_tensor_t"""
+    _fields_ = [("param", _P), ("master", _P), ("grad", _P), ("exp_avg", _P), ("exp_avg_sq", _P),
+                ("exp_avg_scale", _P), ("exp_avg_sq_scale", _P), ("numel", _L)]
+
+
+SIGNATURES = {
+    "adamw_step": ([ctypes.POINTER(AdamWTensor), _I, _I, _I, _I, _D, _D, _D, _D, _D, _L, _P, _P, ctypes.c_uint, _P], _I),
+}
+
+ADAMW_QUANT = 256  # elements that share a scale in an 8-bit state
+
+
+def _overlap(tensors):
+    """Whether two of the (contiguous) tensors share memory."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors if t.numel())
+    return any(b[0] < a[1] for a, b in zip(spans, spans[1:]))
+
+
+class AdamWB200:
+    """AdamW for ``params``: contiguous, 16-byte aligned CUDA tensors of one dtype (bf16 or fp32) on one device.
+
+    ``state_bits``: 32 (fp32 states) or 8 (e4m3 and e5m2 codes with a power of two for each 256 elements, rounded by
+    chance from ``seed``).  ``masters``: for bf16 weights, None (the weights themselves are updated, rounded to nearest),
+    True (fp32 copies are made), or a list of fp32 tensors.  ``step_device``: an int64 CUDA tensor of one element that
+    holds the number of the step to come, for steps captured into a graph; the caller counts it up.  Otherwise
+    ``step_count`` counts the steps taken.
+
+    The states lie in one buffer each, a tensor at a multiple of 256 elements: ``flat["m"]``, ``flat["v"]`` and, with 8
+    bits, ``flat["m_scale"]``, ``flat["v_scale"]``; ``exp_avg`` and ``exp_avg_sq`` are views of them for each tensor.  Saving
+    and restoring ``flat`` and ``step_count`` saves and restores the optimizer."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, state_bits=32, masters=None,
+                 seed=0, step_device=None):
+        import torch
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("there are no weights")
+        first = self.params[0]
+        self.device, self.torch_dtype, self.dtype = first.device, first.dtype, _dtype_code(first.dtype)
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        for p in self.params:
+            self._like(p, "a weight", first.dtype)
+        if masters is not None and first.dtype != torch.bfloat16:
+            raise ValueError("fp32 weights are their own master weights")
+        if masters is True:
+            masters = [p.detach().float() for p in self.params]
+        self.masters = None if masters is None else list(masters)
+        if self.masters is not None:
+            if [m.numel() for m in self.masters] != [p.numel() for p in self.params]:
+                raise ValueError("masters must have the weights' sizes")
+            for m in self.masters:
+                self._like(m, "a master weight", torch.float32)
+        if _overlap(self.params + (self.masters or [])):
+            raise ValueError("two weights share memory")
+        if step_device is not None and (step_device.dtype != torch.int64 or step_device.numel() != 1 or
+                                        step_device.device != self.device):
+            raise ValueError(f"step_device must be one int64 element on {self.device}")
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.state_bits, self.seed, self.step_device, self.step_count = state_bits, seed, step_device, 0
+        self._sizes = [p.numel() for p in self.params]
+        at, starts = 0, []
+        for n in self._sizes:
+            starts.append(at)
+            at += -(-n // ADAMW_QUANT) * ADAMW_QUANT
+        new = lambda n, dtype: torch.zeros(n, dtype=torch.uint8 if dtype != torch.float32 else dtype,  # noqa: E731
+                                           device=self.device).view(dtype)
+        m_type, v_type = (torch.float8_e4m3fn, torch.float8_e5m2) if state_bits == 8 else (torch.float32, torch.float32)
+        self.flat = {"m": new(at, m_type), "v": new(at, v_type)}
+        if state_bits == 8:
+            for name in ("m_scale", "v_scale"):
+                self.flat[name] = torch.ones(at // ADAMW_QUANT, dtype=torch.float32, device=self.device)
+        views = lambda name: [self.flat[name][s:s + n] for s, n in zip(starts, self._sizes)]  # noqa: E731
+        self.exp_avg, self.exp_avg_sq = views("m"), views("v")
+        self._table = (AdamWTensor * len(self.params))()
+        for i, (p, start) in enumerate(zip(self.params, starts)):
+            e = self._table[i]
+            e.param, e.numel = p.data_ptr(), p.numel()
+            e.master = None if self.masters is None else self.masters[i].data_ptr()
+            e.exp_avg, e.exp_avg_sq = self.exp_avg[i].data_ptr(), self.exp_avg_sq[i].data_ptr()
+            if state_bits == 8:
+                e.exp_avg_scale = self.flat["m_scale"].data_ptr() + 4 * (start // ADAMW_QUANT)
+                e.exp_avg_sq_scale = self.flat["v_scale"].data_ptr() + 4 * (start // ADAMW_QUANT)
+
+    def _like(self, t, what, dtype):
+        if not t.is_cuda or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous CUDA tensor on {self.device}")
+        if t.dtype != dtype:
+            raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+
+    def step(self, grads, lr=None, grad_scale=None, stream=None):
+        """One step with ``grads``, a gradient (bf16 or fp32, one dtype) for each weight.  ``grad_scale``: a
+        one-element fp32 CUDA tensor that multiplies them; where it is not finite or not above zero nothing
+        changes.  ``lr``: this step's rate instead of the optimizer's."""
+        import torch
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(self.params)} gradients are wanted, {len(grads)} given")
+        dtype, device, table = grads[0].dtype, self.device, self._table
+        code = _dtype_code(dtype)
+        for i, (g, n) in enumerate(zip(grads, self._sizes)):
+            if g.numel() != n or g.dtype != dtype or g.device != device or not g.is_contiguous():
+                raise ValueError(f"gradient {i} must be a contiguous {dtype} tensor of {n} elements on {device}")
+            table[i].grad = g.data_ptr()
+        scale = None
+        if grad_scale is not None:
+            if grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or grad_scale.device != device:
+                raise ValueError(f"grad_scale must be one fp32 element on {device}")
+            scale = grad_scale.data_ptr()
+        counter = None if self.step_device is None else self.step_device.data_ptr()
+        _on(self.params[0], stream, lambda s: _check(load().adamw_step(
+            table, len(table), self.dtype, code, self.state_bits, self.lr if lr is None else lr, self.betas[0],
+            self.betas[1], self.eps, self.weight_decay, self.step_count + 1, counter, scale, self.seed & 0xFFFFFFFF, s)))
+        self.step_count += 1

@@ -1,0 +1,352 @@
+"""Operators over sequences: the causal depthwise convolution over time and the gated
+linear recurrence, a thin binding of ``include/sequence_b200.h``.
+
+Tensors over sequences are (B, T, C), or (rows, C) with ``offsets`` (B + 1 int32 values on the
+device): sequences of their own lengths packed one behind the other.  Channels are contiguous
+and rows a fixed distance apart, so a slice ``z[..., :C]`` of a wider projection is taken as it is.
+
+``CausalConv1dB200`` and ``GatedRecurrenceB200`` hold a layer's weights; a call is the forward
+pass, ``backward`` its gradients, ``step`` one token for each of a batch of sequences.  Scratch is
+allocated for each call on the call's stream, so calls on several streams, and graphs captured
+from them, share none.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _check, _dtype_code, load
+
+CONV_ACT_NONE = 0
+CONV_ACT_SILU = 1
+
+_I, _P, _S, _L, _F = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_longlong, ctypes.c_float
+_SEQ = [_P, _I, _I, _L, _I]  # offsets, nseq, T, rows, C
+SIGNATURES = {
+    "conv1d_causal_forward": ([_P] * 6 + _SEQ + [_I, _I, _L, _L, _I, _P], _I),
+    "conv1d_causal_backward_workspace_size": ([_L, _I, _I, ctypes.POINTER(_S)], _I),
+    "conv1d_causal_backward": ([_P] * 10 + _SEQ + [_I, _I, _L, _L, _L, _I, _P, _S, _P], _I),
+    "conv1d_causal_step": ([_P] * 6 + [_I] * 5 + [_L, _L, _I, _P], _I),
+    "gated_recurrence_saved_size": ([_L, _I, ctypes.POINTER(_S)], _I),
+    "gated_recurrence_workspace_size": ([_L, _I, ctypes.POINTER(_S)], _I),
+    "gated_recurrence_backward_workspace_size": ([_L, _I, ctypes.POINTER(_S)], _I),
+    "gated_recurrence_forward": ([_P] * 4 + [_F] + [_P] * 4 + _SEQ + [_L] * 4 + [_I, _P, _S, _P], _I),
+    "gated_recurrence_backward": ([_P] * 4 + [_F] + [_P] * 9 + _SEQ + [_L] * 7 + [_I, _P, _S, _P], _I),
+    "gated_recurrence_step": ([_P] * 4 + [_F] + [_P] * 3 + [_I] * 3 + [_L] * 4 + [_I, _P], _I),
+}
+
+
+def _size(fn, *args) -> int:
+    out = ctypes.c_size_t(0)
+    _check(fn(*args, ctypes.byref(out)))
+    return out.value
+
+
+def conv1d_causal_backward_workspace_size(rows, C, K) -> int:
+    return _size(load().conv1d_causal_backward_workspace_size, rows, C, K)
+
+
+def gated_recurrence_saved_size(rows, C) -> int:
+    return _size(load().gated_recurrence_saved_size, rows, C)
+
+
+def gated_recurrence_workspace_size(rows, C) -> int:
+    return _size(load().gated_recurrence_workspace_size, rows, C)
+
+
+def gated_recurrence_backward_workspace_size(rows, C) -> int:
+    return _size(load().gated_recurrence_backward_workspace_size, rows, C)
+
+
+# ------------------------------------------------------------ argument checks ---
+def _rows(name, t, like, shape=None, dtype=None):
+    """(pointer, row stride) of a tensor over rows: on `like`'s device, of `like`'s shape and dtype
+    unless others are given."""
+    if t.device != like.device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {like.device}, not on {t.device}")
+    if t.dtype != (dtype or like.dtype):
+        raise TypeError(f"{name} must be {dtype or like.dtype}, not {t.dtype}")
+    if t.shape != (shape or like.shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape or like.shape)}, not {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), t.shape[-1]
+    stride, sizes = t.stride(), t.shape
+    if sizes[-1] > 1 and stride[-1] != 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+    if t.dim() == 2:
+        return t.data_ptr(), stride[0] if sizes[0] > 1 else max(stride[0], sizes[1])
+    B, T, C = sizes
+    if T > 1:
+        if B > 1 and stride[0] != T * stride[1]:
+            raise ValueError(f"the rows of {name} must lie a fixed distance apart; use {name}.contiguous()")
+        return t.data_ptr(), stride[1]
+    return t.data_ptr(), stride[0] if B > 1 else max(stride[0], C)
+
+
+def _whole(name, t, shape, dtype, device):
+    """Pointer of a contiguous tensor of exactly this shape and type (None: no tensor)."""
+    if t is None:
+        return None
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _sequences(x, offsets):
+    """(offsets pointer, number of sequences, T, rows, C) of an input over sequences."""
+    import torch
+    if offsets is None:
+        if x.dim() != 3:
+            raise ValueError("without offsets, x must be (B, T, C)")
+        B, T, C = x.shape
+        return None, B, T, B * T, C
+    if x.dim() != 2:
+        raise ValueError("with offsets, x must be (rows, C)")
+    if offsets.dim() != 1 or offsets.numel() < 2 or offsets.dtype != torch.int32:
+        raise ValueError("offsets must hold one int32 value more than there are sequences")
+    if offsets.device != x.device or not offsets.is_contiguous():
+        raise ValueError(f"offsets must be a contiguous tensor on {x.device}")
+    return offsets.data_ptr(), offsets.numel() - 1, 0, x.shape[0], x.shape[1]
+
+
+def _on(x, stream, call):
+    """call(raw stream) with x's device current, and `stream` (a torch stream or a handle) where
+    one is given, so that what the call allocates belongs to the stream it is used on."""
+    import torch
+    if not x.is_cuda:
+        raise ValueError("tensors passed to the library must be CUDA tensors")
+    if stream is None and torch.cuda.current_device() == x.device.index:
+        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(x.device):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=x.device) if stream else torch.cuda.default_stream(x.device)
+        if stream.device != x.device:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {x.device}")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+def _slots(slots, B, device):
+    import torch
+    return _whole("slots", slots, (B,), torch.int32, device)
+
+
+def _scratch(nbytes, device):
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+# ----------------------------------------------------------------- convolution ---
+class CausalConv1dB200:
+    """A causal depthwise convolution over time: y[t] = act(bias + sum_k w[:, k] x[t-K+1+k]).
+
+    ``w`` is (C, K) with 2 <= K <= 8, ``bias`` (C,) or None, both bf16 or fp32 on one CUDA device;
+    ``activation`` is None or "silu".  The layer reads the tensors it was given: updating
+    them in place (``AdamWB200`` does) updates the layer."""
+
+    def __init__(self, w, bias=None, activation=None):
+        if w.dim() != 2:
+            raise ValueError("w must be (C, K)")
+        if not 2 <= w.shape[1] <= 8:
+            raise ValueError("K must lie in 2 .. 8")
+        if activation not in (None, "silu"):
+            raise ValueError(f"unknown activation {activation!r}; use None or 'silu'")
+        self.C, self.K = int(w.shape[0]), int(w.shape[1])
+        self.dtype = _dtype_code(w.dtype)
+        self.torch_dtype, self.device = w.dtype, w.device
+        _whole("w", w, w.shape, w.dtype, w.device)
+        _whole("bias", bias, (self.C,), w.dtype, w.device)
+        self.w, self.bias = w, bias
+        self.act = CONV_ACT_SILU if activation == "silu" else CONV_ACT_NONE
+
+    def _input(self, x):
+        if x.shape[-1] != self.C:
+            raise ValueError(f"x has {x.shape[-1]} channels, the layer {self.C}")
+        if x.dtype != self.torch_dtype:
+            raise TypeError(f"x must be {self.torch_dtype}, not {x.dtype}")
+        if x.device != self.device:
+            raise ValueError(f"x must be on {self.device}, not on {x.device}")
+
+    def __call__(self, x, y=None, offsets=None, initial_state=None, final_state=None, stream=None):
+        """y for x (B, T, C), or (rows, C) with offsets.  ``initial_state`` (B, K-1, C): the rows before each
+        sequence; ``final_state``: a buffer of that shape that receives its last K-1 rows."""
+        import torch
+        self._input(x)
+        seq = _sequences(x, offsets)
+        window = (seq[1], self.K - 1, self.C)
+        px, ldx = _rows("x", x, x)
+        state = _whole("initial_state", initial_state, window, x.dtype, x.device)
+        final = _whole("final_state", final_state, window, x.dtype, x.device)
+
+        def call(s):
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+            py, ldy = _rows("y", out, x)
+            _check(load().conv1d_causal_forward(px, self.w.data_ptr(), self._bias(), py, state, final, *seq, self.K,
+                                                self.act, ldx, ldy, self.dtype, s))
+            return out
+        return _on(x, stream, call)
+
+    def _bias(self):
+        return None if self.bias is None else self.bias.data_ptr()
+
+    def backward(self, x, dy, offsets=None, initial_state=None, d_final_state=None, dx=None, dw=None, db=None,
+                 d_initial_state=None, stream=None):
+        """(dx, dw, db, d_initial_state) for the forward pass's arguments and dy; db without a bias and
+        d_initial_state without an initial state are None."""
+        import torch
+        self._input(x)
+        seq = _sequences(x, offsets)
+        window = (seq[1], self.K - 1, self.C)
+        px, ldx = _rows("x", x, x)
+        pdy, lddy = _rows("dy", dy, x)
+        state = _whole("initial_state", initial_state, window, x.dtype, x.device)
+        dfinal = _whole("d_final_state", d_final_state, window, x.dtype, x.device)
+
+        def call(s):
+            empty = lambda *shape: torch.empty(shape, dtype=x.dtype, device=x.device)  # noqa: E731
+            gx = empty(*x.shape) if dx is None else dx
+            gw = empty(self.C, self.K) if dw is None else dw
+            gb = empty(self.C) if db is None and self.bias is not None else db
+            gs = empty(*window) if d_initial_state is None and initial_state is not None else d_initial_state
+            pgx, ldgx = _rows("dx", gx, x)
+            ws = _scratch(conv1d_causal_backward_workspace_size(seq[3], self.C, self.K), x.device)
+            _check(load().conv1d_causal_backward(
+                px, self.w.data_ptr(), self._bias(), pdy, state, dfinal, pgx,
+                _whole("dw", gw, (self.C, self.K), x.dtype, x.device), _whole("db", gb, (self.C,), x.dtype, x.device),
+                _whole("d_initial_state", gs, window, x.dtype, x.device), *seq, self.K, self.act, ldx, lddy, ldgx,
+                self.dtype, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), s))
+            return gx, gw, gb, gs
+        return _on(x, stream, call)
+
+    def step(self, x, state, slots=None, y=None, stream=None):
+        """One token for each of B sequences: y (B, C) for x (B, C), and the windows in ``state`` (pool, K-1, C)
+        moved on in place.  Row b's window is state[slots[b]] (int32; outside the pool: no sequence, y's row stays
+        as it was), or state[b] without slots."""
+        import torch
+        self._input(x)
+        if x.dim() != 2:
+            raise ValueError("x must be (B, C)")
+        B = x.shape[0]
+        px, ldx = _rows("x", x, x)
+        ps = _whole("state", state, (state.shape[0], self.K - 1, self.C), x.dtype, x.device)
+        pslots = _slots(slots, B, x.device)
+
+        def call(s):
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+            py, ldy = _rows("y", out, x)
+            _check(load().conv1d_causal_step(px, self.w.data_ptr(), self._bias(), py, ps, pslots, B, state.shape[0],
+                                             self.C, self.K, self.act, ldx, ldy, self.dtype, s))
+            return out
+        return _on(x, stream, call)
+
+
+# ------------------------------------------------------------------ recurrence ---
+class GatedRecurrenceB200:
+    """The gated linear recurrence h[t] = a h[t-1] + sqrt(1 - a^2) sigmoid(gate_x) x with
+    a = exp(-kappa softplus(decay) sigmoid(gate_a)), each channel by itself.
+
+    ``decay`` is (C,) fp32; x and the gates are bf16 or fp32 of one shape; states are fp32.  The
+    layer reads the ``decay`` it was given: updating it in place updates the layer."""
+
+    def __init__(self, decay, kappa=8.0):
+        import torch
+        if decay.dim() != 1:
+            raise ValueError("decay must be (C,)")
+        _whole("decay", decay, decay.shape, torch.float32, decay.device)
+        self.decay, self.kappa, self.C, self.device = decay, float(kappa), int(decay.shape[0]), decay.device
+
+    def _input(self, x):
+        if x.shape[-1] != self.C:
+            raise ValueError(f"x has {x.shape[-1]} channels, the layer {self.C}")
+        if x.device != self.device:
+            raise ValueError(f"x must be on {self.device}, not on {x.device}")
+        return _dtype_code(x.dtype)
+
+    def saved_states(self, x):
+        """A buffer for the states that the forward pass over x saves for its backward pass."""
+        import torch
+        rows = x.numel() // max(1, x.shape[-1])
+        return torch.empty(gated_recurrence_saved_size(rows, self.C) // 4, dtype=torch.float32, device=x.device)
+
+    def _saved(self, saved, rows, device):
+        import torch
+        return _whole("saved", saved, (gated_recurrence_saved_size(rows, self.C) // 4,), torch.float32, device)
+
+    def __call__(self, x, gate_a, gate_x, y=None, offsets=None, initial_state=None, final_state=None, saved=None,
+                 stream=None):
+        """y = h for x (B, T, C), or (rows, C) with offsets.  ``initial_state`` (B, C): h before each sequence;
+        ``final_state``: a buffer of that shape that receives its last h; ``saved``: ``saved_states(x)``, filled for
+        ``backward``."""
+        import torch
+        code = self._input(x)
+        seq = _sequences(x, offsets)
+        (px, ldx), (pa, lda), (pg, ldg) = _rows("x", x, x), _rows("gate_a", gate_a, x), _rows("gate_x", gate_x, x)
+        state = _whole("initial_state", initial_state, (seq[1], self.C), torch.float32, x.device)
+        final = _whole("final_state", final_state, (seq[1], self.C), torch.float32, x.device)
+        psaved = None if saved is None else self._saved(saved, seq[3], x.device)
+
+        def call(s):
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+            py, ldy = _rows("y", out, x)
+            ws = _scratch(gated_recurrence_workspace_size(seq[3], self.C), x.device)
+            _check(load().gated_recurrence_forward(
+                px, pa, pg, self.decay.data_ptr(), self.kappa, py, state, final, psaved, *seq, ldx, lda, ldg, ldy, code,
+                None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), s))
+            return out
+        return _on(x, stream, call)
+
+    def backward(self, x, gate_a, gate_x, dy, saved, offsets=None, initial_state=None, d_final_state=None, dx=None,
+                 d_gate_a=None, d_gate_x=None, d_decay=None, d_initial_state=None, stream=None):
+        """(dx, d_gate_a, d_gate_x, d_decay, d_initial_state) for the forward pass's arguments, the ``saved`` it
+        filled, and dy; d_initial_state is None without an initial state."""
+        import torch
+        code = self._input(x)
+        seq = _sequences(x, offsets)
+        (px, ldx), (pa, lda), (pg, ldg) = _rows("x", x, x), _rows("gate_a", gate_a, x), _rows("gate_x", gate_x, x)
+        pdy, lddy = _rows("dy", dy, x)
+        f32 = torch.float32
+        state = _whole("initial_state", initial_state, (seq[1], self.C), f32, x.device)
+        dfinal = _whole("d_final_state", d_final_state, (seq[1], self.C), f32, x.device)
+        psaved = self._saved(saved, seq[3], x.device)
+
+        def call(s):
+            like = lambda t: torch.empty(x.shape, dtype=x.dtype, device=x.device) if t is None else t  # noqa: E731
+            gx, ga, gg = like(dx), like(d_gate_a), like(d_gate_x)
+            gd = torch.empty(self.C, dtype=f32, device=x.device) if d_decay is None else d_decay
+            gs = d_initial_state
+            if gs is None and initial_state is not None:
+                gs = torch.empty(seq[1], self.C, dtype=f32, device=x.device)
+            (pgx, ldgx), (pga, ldga), (pgg, ldgg) = _rows("dx", gx, x), _rows("d_gate_a", ga, x), _rows("d_gate_x", gg, x)
+            ws = _scratch(gated_recurrence_backward_workspace_size(seq[3], self.C), x.device)
+            _check(load().gated_recurrence_backward(
+                px, pa, pg, self.decay.data_ptr(), self.kappa, pdy, psaved, state, dfinal, pgx, pga, pgg,
+                _whole("d_decay", gd, (self.C,), f32, x.device),
+                _whole("d_initial_state", gs, (seq[1], self.C), f32, x.device), *seq, ldx, lda, ldg, lddy, ldgx, ldga,
+                ldgg, code, ws.data_ptr(), ws.numel(), s))
+            return gx, ga, gg, gd, gs
+        return _on(x, stream, call)
+
+    def step(self, x, gate_a, gate_x, state, slots=None, y=None, stream=None):
+        """One token for each of B sequences: y (B, C) for x and the gates (B, C); ``state`` (pool, C) fp32 is updated
+        in place, slots as in ``CausalConv1dB200.step``."""
+        import torch
+        code = self._input(x)
+        if x.dim() != 2:
+            raise ValueError("x must be (B, C)")
+        B = x.shape[0]
+        (px, ldx), (pa, lda), (pg, ldg) = _rows("x", x, x), _rows("gate_a", gate_a, x), _rows("gate_x", gate_x, x)
+        ps = _whole("state", state, (state.shape[0], self.C), torch.float32, x.device)
+        pslots = _slots(slots, B, x.device)
+
+        def call(s):
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+            py, ldy = _rows("y", out, x)
+            _check(load().gated_recurrence_step(px, pa, pg, self.decay.data_ptr(), self.kappa, py, ps, pslots, B,
+                                                state.shape[0], self.C, ldx, lda, ldg, ldy, code, s))
+            return out
+        return _on(x, stream, call)

@@ -1,0 +1,255 @@
+"""AdamW on a B200, and the layers and the optimizer as they are used together: a training step of a
+convolution layer and of a sequence block, and the block's tokens after its training.
+
+A weight in fp32 (or its master) is off from the 64-bit step by the roundings of its own value, and by its update's:
+2 u |p| + 16 u lr (|m^| / (sqrt(v^) + eps) + decay |p|); u = 2^-24.  m and v: three products and a sum, 4 u of the sum of
+their terms' sizes.  bf16 adds half a step, 2^-8 of the value."""
+import pytest
+import torch
+
+import cnn_convolution_conv2d_b200 as cb
+import sequence_reference as ref
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda_ready():
+    assert torch.cuda.is_available(), "these tests need a CUDA device"
+    from cnn_convolution_conv2d_b200 import build
+    build.build()
+    cb.load()
+    yield
+    cb.conv2d_sync_status()
+
+
+SHAPES = [(64, 3, 7, 7), (1,), (255,), (256,), (257,), (2049,), (0,), (512, 16, 3, 3), (5,)]
+
+
+def normal(shape, seed, scale=1.0, dtype=F32):
+    gen = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=gen) * scale).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype, master, gtype", [(F32, False, F32), (F32, False, BF), (BF, False, BF), (BF, True, BF), (BF, True, F32)],
+                         ids=["f32", "f32-gbf16", "bf16", "master", "master-gf32"])
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("copies", [1, 7])     # 63 tensors: more than one launch takes
+def test_steps(dtype, master, gtype, bits, copies):
+    shapes = SHAPES * copies
+    params = [normal(s, i, 0.1, dtype) for i, s in enumerate(shapes)]
+    masters = [normal(s, 100 + i, 0.1) for i, s in enumerate(shapes)] if master else None
+    opt = cb.AdamWB200(params, lr=1e-2, betas=(0.9, 0.99), eps=1e-6, weight_decay=0.1, state_bits=bits, masters=masters, seed=5)
+    scale = torch.tensor([0.5], device="cuda")
+    lr, (b1, b2), eps, wd = 1e-2, (0.9, 0.99), 1e-6, 0.1
+    for step in (1, 2, 3):
+        grads = [normal(s, 1000 * step + i, 1.0, gtype) for i, s in enumerate(shapes)]
+        held = lambda i, name: held_state(opt, i, name)  # noqa: E731
+        before = [((masters or params)[i].double().cpu().flatten(), held(i, "m"), held(i, "v")) for i in range(len(shapes))]
+        opt.step(grads, grad_scale=scale if step == 3 else None)
+        for i, (p0, m0, v0) in enumerate(before):
+            g = grads[i].double().cpu().flatten() * (0.5 if step == 3 else 1.0)
+            p, m, v = ref.adamw(p0, g, m0, v0, lr, b1, b2, eps, wd, step)
+            update = (m0.abs() * b1 + g.abs() * (1 - b1)) / (1 - b1 ** step) / ((v / (1 - b2 ** step)).sqrt() + eps)
+            atol = 2 * ref.U * p0.abs() + 16 * ref.U * lr * (update + wd * p0.abs())
+            if master:
+                ref.close(masters[i].flatten(), p, F32, atol, f"master {i}")
+                assert torch.equal(masters[i].to(BF), params[i])
+            else:
+                ref.close(params[i].flatten(), p, dtype, atol, f"weight {i}")
+            terms = b1 * m0.abs() + (1 - b1) * g.abs()
+            if bits == 32:
+                ref.close(opt.exp_avg[i], m, F32, 4 * ref.U * terms, f"m {i}")
+                ref.close(opt.exp_avg_sq[i], v, F32, 4 * ref.U * v, f"v {i}")
+            else:
+                # held between the two codes around the value: less than one step, an eighth of a value in e4m3 and a
+                # quarter in e5m2, or one of the equal steps below the smallest normal number
+                check_codes(opt, i, m, v, terms)
+    cb.conv2d_sync_status()
+
+
+def held_state(opt, i, name):
+    """The values that a tensor's state stands for, in 64 bits."""
+    t = (opt.exp_avg if name == "m" else opt.exp_avg_sq)[i].double().cpu()
+    if opt.state_bits == 32 or not t.numel():
+        return t
+    start = (t.data_ptr() * 0 + (opt.exp_avg if name == "m" else opt.exp_avg_sq)[i].storage_offset()) // 256
+    scale = opt.flat[name + "_scale"][start:start + -(-t.numel() // 256)].double().cpu()
+    return t * scale.repeat_interleave(256)[:t.numel()]
+
+
+def check_codes(opt, i, m, v, terms):
+    for name, value, top, least, rel, sizes in (("m", m, 7, 2.0 ** -9, 2.0 ** -3, terms), ("v", v, 14, 2.0 ** -16, 2.0 ** -2, v)):
+        got = held_state(opt, i, name)
+        if not got.numel():
+            continue
+        start = (opt.exp_avg if name == "m" else opt.exp_avg_sq)[i].storage_offset() // 256
+        scale = opt.flat[name + "_scale"][start:start + -(-got.numel() // 256)].double().cpu()
+        assert bool((torch.log2(scale) == torch.log2(scale).round()).all())
+        # the scale is that of the largest fp32 value, which is off by 4 u of its terms (which may cancel: then it says nothing)
+        block = lambda t: torch.nn.functional.pad(t.abs(), (0, -t.numel() % 256)).view(-1, 256).amax(1)  # noqa: E731
+        big, slack = block(value), 4 * ref.U * block(sizes)
+        inside = ((big >= scale * 2.0 ** top - slack) & (big < scale * 2.0 ** (top + 1) + slack)) | (big <= slack)
+        assert bool(inside.all()), (name, i)
+        wide = scale.repeat_interleave(256)[:got.numel()]
+        allowed = torch.maximum(rel * value.abs(), least * wide) * (1 + 1e-6) + 4 * ref.U * sizes
+        assert bool(((got - value).abs() <= allowed).all()), (name, i)
+        if name == "v":
+            assert bool((got[value > 0] > 0).all())
+
+
+def test_rounding_by_chance_keeps_the_mean():
+    """With beta2 = 0.999 a constant gradient moves v by a thousandth a step: rounding to nearest would leave it; by chance
+    its mean follows.  v after n steps is 1 - beta2^n; a step of chance is a random move of at most a quarter of v, so the mean
+    of N elements is off by less than 6 standard deviations, 6 * 0.25 * sqrt(n / N), of v."""
+    N, n = 1 << 16, 400
+    p = torch.zeros(N, device="cuda")
+    opt = cb.AdamWB200([p], lr=0.0, weight_decay=0.0, state_bits=8, seed=9)
+    g = [torch.ones(N, device="cuda")]
+    for _ in range(n):
+        opt.step(g)
+    v = held_state(opt, 0, "v").mean().item()
+    want = 1 - 0.999 ** n
+    assert abs(v - want) <= 6 * 0.25 * (n / N) ** 0.5 * want
+    m = held_state(opt, 0, "m").mean().item()
+    assert abs(m - 1) <= 6 * 0.125 * (n / N) ** 0.5
+
+
+def test_equal_seeds_give_equal_bits_and_the_device_counter_the_same_steps():
+    def run(seed, device_counter, graph=False):
+        params = [normal((300, 40), 1), normal((77,), 2)]
+        grads = [normal((300, 40), 3), normal((77,), 4)]
+        counter = torch.ones(1, dtype=torch.int64, device="cuda") if device_counter else None
+        opt = cb.AdamWB200(params, state_bits=8, seed=seed, step_device=counter)
+        if graph:
+            opt.step(grads)                     # step 1, and the first launch outside the capture
+            counter += 1
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                opt.step(grads)
+                counter.add_(1)
+            for _ in range(2):
+                g.replay()
+        else:
+            for _ in range(3):
+                opt.step(grads)
+                if device_counter:
+                    counter += 1
+        torch.cuda.synchronize()
+        return [t.clone() for t in params] + [t.view(torch.uint8).clone() for t in (opt.flat["m"], opt.flat["v"])]
+
+    one, two, other = run(1, False), run(1, False), run(2, False)
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
+    assert not torch.equal(one[3], other[3])
+    assert all(torch.equal(a, b) for a, b in zip(one, run(1, True)))
+    assert all(torch.equal(a, b) for a, b in zip(one, run(1, True, graph=True)))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_what_is_not_finite(bits):
+    p = normal((1000,), 1)
+    opt = cb.AdamWB200([p], state_bits=bits)
+    g = normal((1000,), 2)
+    for bad in (0.0, -1.0, float("nan"), float("inf")):      # a scale that is no scale: nothing changes
+        kept = p.clone()
+        opt.step([g], grad_scale=torch.tensor([bad], device="cuda"))
+        assert torch.equal(p, kept) and bool((opt.flat["m"].float() == 0).all())
+    clean = cb.AdamWB200([normal((1000,), 1)], state_bits=bits)
+    clean.step_count = opt.step_count
+    clean.step([g])
+    spoilt = g.clone()
+    spoilt[300], spoilt[301] = float("nan"), float("inf")
+    opt.step([spoilt])
+    mask = torch.ones(1000, dtype=torch.bool, device="cuda")
+    mask[300:302] = False
+    assert bool(p[300:302].isnan().all()) and torch.equal(p[mask], clean.params[0][mask])
+    assert bool(opt.exp_avg[0].float()[300:302].isnan().all() if bits == 8 else ~opt.exp_avg[0][300:302].isfinite().any())
+    # the spoilt elements leave the scale to the others
+    assert torch.equal(opt.exp_avg[0].float()[:256], clean.exp_avg[0].float()[:256])
+    assert bool(opt.exp_avg[0].float()[mask].isfinite().all()) and bool(opt.exp_avg_sq[0].float()[mask].isfinite().all())
+
+
+def test_refusals():
+    p = [torch.zeros(16, device="cuda"), torch.zeros(16, device="cuda")]
+    for bad in (lambda: cb.AdamWB200([p[0], p[0]]), lambda: cb.AdamWB200([p[0], p[0][4:12]]), lambda: cb.AdamWB200(p, state_bits=4),
+                lambda: cb.AdamWB200(p, masters=True), lambda: cb.AdamWB200([torch.zeros(4, 4, device="cuda").t()]),
+                lambda: cb.AdamWB200(p, step_device=torch.zeros(1, device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    opt = cb.AdamWB200(p)
+    for bad in ([p[0]], [p[0], torch.zeros(15, device="cuda")], [p[0], torch.zeros(16)], [p[0], torch.zeros(16, device="cuda", dtype=BF)]):
+        with pytest.raises(ValueError):
+            opt.step(bad)
+    with pytest.raises(TypeError):
+        cb.AdamWB200([p[0], torch.zeros(4, device="cuda", dtype=BF)])
+    with pytest.raises(cb.Conv2dError) as err:
+        opt.step(p, lr=-1.0)
+    assert err.value.status == cb.CONV_ERR_INVALID_ARG
+    assert opt.step_count == 0
+    unaligned = cb.AdamWB200([torch.zeros(40, device="cuda")[1:33]])
+    with pytest.raises(cb.Conv2dError) as err:
+        unaligned.step([p[0].repeat(2)])
+    assert err.value.status == cb.CONV_ERR_UNSUPPORTED
+
+
+def test_training_a_convolution_layer():
+    """Forward, backward, AdamW and again: the layer's own gradients update the weights it packs."""
+    w, b = normal((16, 8, 3, 3), 1, 0.1), normal((16,), 2, 0.1)
+    x, dy = normal((2, 8, 9, 9), 3), normal((2, 16, 9, 9), 4)
+    layer = cb.Conv2dB200(w, b, pad=1, layout="nchw")
+    opt = cb.AdamWB200([w, b], lr=1e-2)
+    dx0 = layer.backward_data(dy, 9, 9)
+    dw, db = layer.backward_weight(x, dy)
+    before = [t.double().cpu().flatten() for t in (w, b, dw, db)]
+    opt.step([dw, db])
+    for t, p, g in ((w, before[0], before[2]), (b, before[1], before[3])):
+        want, _, _ = ref.adamw(p, g, 0 * g, 0 * g, 1e-2, 0.9, 0.999, 1e-8, 1e-2, 1)
+        ref.close(t.flatten(), want, F32, 2 * ref.U * p.abs() + 16 * ref.U * 1e-2 * (1 + 1e-2 * p.abs()))
+    layer.repack()
+    fresh = cb.Conv2dB200(w.clone(), b.clone(), pad=1, layout="nchw")
+    assert torch.equal(layer(x), fresh(x))
+    dx1 = layer.backward_data(dy, 9, 9)
+    assert torch.equal(dx1, fresh.backward_data(dy, 9, 9)) and not torch.equal(dx0, dx1)
+    cb.conv2d_sync_status()
+
+
+def test_a_sequence_block_from_training_to_tokens():
+    """Convolution, recurrence, their gradients and AdamW as a training step uses them, on packed sequences; then a prompt
+    and single tokens with the trained weights, against one pass over all of it."""
+    C, K, off = 96, 4, [0, 70, 70, 300]
+    x, dh = normal((300, C), 1), normal((300, C), 2)
+    gates = normal((300, 2 * C), 3)
+    w, b, decay = normal((C, K), 4, 0.5), normal((C,), 5), normal((C,), 6) - 3
+    conv, rec = cb.CausalConv1dB200(w, b, "silu"), cb.GatedRecurrenceB200(decay)
+    opt = cb.AdamWB200([w, b, decay], lr=1e-2, state_bits=32)
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+    ga, gx = gates[:, :C], gates[:, C:]
+    wide = [t.double().cpu().requires_grad_() for t in (w, b, decay)]
+    for step in (1, 2):
+        y = conv(x, offsets=offsets)
+        saved = rec.saved_states(y)
+        rec(y, ga, gx, offsets=offsets, saved=saved)
+        dy, _, _, ddecay, _ = rec.backward(y, ga, gx, dh, saved, offsets=offsets)
+        _, dw, db, _ = conv.backward(x, dy, offsets=offsets)
+        wide = [t.double().cpu().requires_grad_() for t in (w, b, decay)]
+        seqs = ref.pieces(x.shape, off)
+        yy, _, _ = ref.conv1d(x.double().cpu(), wide[0], wide[1], True, seqs)
+        hh, _, _ = ref.recurrence(yy, ga.double().cpu(), gx.double().cpu(), wide[2], 8.0, seqs)
+        wanted = torch.autograd.grad((hh * dh.double().cpu()).sum(), wide)
+        for name, got, want in zip(("dw", "db", "ddecay"), (dw, db, ddecay), wanted):
+            # two operators in a row: twice the bar of one
+            ref.close(got, want, F32, 2 * ref.GRAD * want.abs().max().item(), name)
+        opt.step([dw, db, ddecay])
+    # the layers read the updated weights: a prompt of 50 rows each, then one token at a time
+    xs, gs = normal((2, 60, C), 7), normal((2, 60, 2 * C), 8)
+    whole = rec(conv(xs), gs[..., :C], gs[..., C:])
+    window, state = torch.zeros(2, K - 1, C, device="cuda"), torch.zeros(2, C, device="cuda")
+    y = conv(xs[:, :50].contiguous(), final_state=window)
+    rec(y, gs[:, :50, :C].contiguous(), gs[:, :50, C:].contiguous(), final_state=state)
+    for t in range(50, 60):
+        y = conv.step(xs[:, t], window)
+        h = rec.step(y, gs[:, t, :C], gs[:, t, C:], state)
+        scale = whole[:, t].abs().max().item()
+        ref.close(h, whole[:, t].double().cpu(), F32, ref.GRAD * scale, f"token {t}")
+    cb.conv2d_sync_status()

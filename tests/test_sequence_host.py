@@ -1,0 +1,209 @@
+"""The operators over sequences and AdamW without a GPU: the headers, the sizes, and the refusals, which come
+before anything touches the device."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import cnn_convolution_conv2d_b200 as cb
+from cnn_convolution_conv2d_b200 import optimizer, sequence
+import sequence_reference as ref
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+TABLES = {"sequence_b200.h": sequence.SIGNATURES, "optimizer_b200.h": optimizer.SIGNATURES}
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from cnn_convolution_conv2d_b200 import build
+    build.build()
+    return cb.load()
+
+
+@pytest.mark.parametrize("header", sorted(TABLES))
+def test_headers_and_signatures_agree(lib, header):
+    text = open(os.path.join(ROOT, "include", header), encoding="utf-8").read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    decls = {n: len(a.split(",")) for n, a in re.findall(r"^int\s+(\w+)\s*\(([^)]*)\)\s*;", text, flags=re.M)}
+    assert set(decls) == set(TABLES[header])
+    for name, count in decls.items():
+        assert len(TABLES[header][name][0]) == count, name
+        assert hasattr(lib, name)
+
+
+def test_adamw_struct_matches_the_header():
+    # seven pointers and a long long: no padding on a 64-bit machine
+    assert ctypes.sizeof(optimizer.AdamWTensor) == 64
+
+
+def test_sizes(lib):
+    assert cb.conv1d_causal_backward_workspace_size(0, 64, 4) == 0
+    # without a device strips are 64 rows, four to a block: 1000 rows are 4 blocks of (K + 1) C sums
+    if not torch.cuda.is_available():
+        assert cb.conv1d_causal_backward_workspace_size(1000, 64, 4) == 4 * 5 * 64 * 4
+    # one chunk: nothing to join; a state for each chunk and channel (rounded up to 64) otherwise
+    assert cb.gated_recurrence_workspace_size(128, 100) == 0
+    assert cb.gated_recurrence_saved_size(129, 100) == 2 * 128 * 4
+    assert cb.gated_recurrence_workspace_size(129, 100) == 256 + 2 * 128 * 12
+    assert cb.gated_recurrence_backward_workspace_size(129, 100) == 256 + 2 * 128 * 16
+    for bad in ((-1, 4), (5, 0)):
+        with pytest.raises(cb.Conv2dError) as err:
+            cb.gated_recurrence_saved_size(*bad)
+        assert err.value.status == cb.CONV_ERR_INVALID_ARG
+    with pytest.raises(cb.Conv2dError) as err:
+        cb.gated_recurrence_workspace_size(2 ** 31, 4)
+    assert err.value.status == cb.CONV_ERR_UNSUPPORTED
+    for K in (1, 9):
+        with pytest.raises(cb.Conv2dError):
+            cb.conv1d_causal_backward_workspace_size(8, 8, K)
+
+
+BF, F = cb.CONV_BF16, cb.CONV_F32
+INVALID, UNSUPPORTED = cb.CONV_ERR_INVALID_ARG, cb.CONV_ERR_UNSUPPORTED
+
+
+def conv_forward(lib, x=16, w=16, bias=None, y=64, state=None, final=None, off=None, nseq=2, T=4, rows=8, C=8, K=4, act=0,
+                 ldx=8, ldy=8, dtype=BF):
+    return lib.conv1d_causal_forward(x, w, bias, y, state, final, off, nseq, T, rows, C, K, act, ldx, ldy, dtype, None)
+
+
+@pytest.mark.parametrize("change, status", [
+    (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(y=None), INVALID), (dict(y=16), INVALID),
+    (dict(nseq=0), INVALID), (dict(T=3), INVALID), (dict(rows=-1), INVALID), (dict(C=0), INVALID), (dict(K=1), INVALID),
+    (dict(K=9), INVALID), (dict(act=2), INVALID), (dict(ldx=-1), INVALID), (dict(ldy=7), INVALID), (dict(dtype=5), INVALID),
+    (dict(state=128, final=128), INVALID), (dict(x=17), UNSUPPORTED), (dict(off=18), UNSUPPORTED),
+    (dict(rows=2 ** 31, T=2 ** 30), UNSUPPORTED),
+], ids=str)
+def test_convolution_refusals(lib, change, status):
+    assert conv_forward(lib, **change) == status
+    assert cb.conv2d_last_error()
+
+
+def test_convolution_backward_refusals(lib):
+    def call(x=16, w=16, dy=32, dx=64, dw=96, ldx=8, dfinal=None, dstate=None, ws=None, nbytes=0, K=4):
+        return lib.conv1d_causal_backward(x, w, None, dy, None, dfinal, dx, dw, None, dstate, None, 2, 4, 8, 8, K, 0, ldx, 8, 8, BF,
+                                          ws, nbytes, None)
+    for change in (dict(dy=None), dict(dx=None), dict(dw=None), dict(dx=32), dict(ldx=-8), dict(K=12),
+                   dict(dfinal=128, dstate=128)):
+        assert call(**change) == INVALID, change
+    assert call(dy=33) == UNSUPPORTED
+
+
+def test_step_refusals(lib):
+    def conv(x=16, w=16, y=64, state=128, slots=None, B=2, pool=2, C=8, K=4, act=0, ldx=8, ldy=8, dtype=BF):
+        return lib.conv1d_causal_step(x, w, None, y, state, slots, B, pool, C, K, act, ldx, ldy, dtype, None)
+    for change in (dict(x=None), dict(w=None), dict(y=None), dict(state=None), dict(B=0), dict(pool=0), dict(pool=1),
+                   dict(C=0), dict(K=1), dict(act=-1), dict(ldy=4), dict(y=16), dict(state=64), dict(dtype=9)):
+        assert conv(**change) == INVALID, change
+    assert conv(slots=129) == UNSUPPORTED
+
+    def rec(x=16, ga=16, gx=16, decay=16, kappa=8.0, y=64, state=128, slots=None, B=2, pool=2, C=8, ldy=8, dtype=BF):
+        return lib.gated_recurrence_step(x, ga, gx, decay, kappa, y, state, slots, B, pool, C, 8, 8, 8, ldy, dtype, None)
+    for change in (dict(x=None), dict(ga=None), dict(gx=None), dict(decay=None), dict(kappa=0.0), dict(kappa=float("inf")),
+                   dict(kappa=float("nan")), dict(state=None), dict(B=0), dict(pool=1), dict(ldy=7), dict(state=64)):
+        assert rec(**change) == INVALID, change
+    assert rec(decay=18) == UNSUPPORTED
+
+
+def test_recurrence_refusals(lib):
+    def forward(x=16, ga=32, gx=48, decay=16, kappa=8.0, y=64, state=None, final=None, off=None, nseq=2, T=4, rows=8, C=8,
+                lda=8, ldy=8, dtype=BF, ws=None, nbytes=0):
+        return lib.gated_recurrence_forward(x, ga, gx, decay, kappa, y, state, final, None, off, nseq, T, rows, C, 8, lda, 8,
+                                            ldy, dtype, ws, nbytes, None)
+    for change in (dict(x=None), dict(ga=None), dict(gx=None), dict(decay=None), dict(y=None), dict(y=32), dict(kappa=-1.0),
+                   dict(nseq=0), dict(T=5), dict(C=0), dict(lda=-2), dict(ldy=4), dict(dtype=3), dict(state=96, final=96)):
+        assert forward(**change) == INVALID, change
+    assert forward(gx=49) == UNSUPPORTED
+    # more than one chunk: the workspace is checked, before any device is asked for
+    assert forward(T=128, rows=256) == cb.CONV_ERR_WORKSPACE
+    assert forward(T=128, rows=256, ws=256, nbytes=100) == cb.CONV_ERR_WORKSPACE
+    assert forward(T=128, rows=256, ws=264, nbytes=1 << 20) == UNSUPPORTED
+
+    def backward(saved=256, dx=64, dga=128, dgx=192, ddecay=16, ws=None, nbytes=0):
+        return lib.gated_recurrence_backward(16, 32, 48, 512, 8.0, 56, saved, None, None, dx, dga, dgx, ddecay, None, None, 2, 4,
+                                             8, 8, 8, 8, 8, 8, 8, 8, 8, BF, ws, nbytes, None)
+    for change in (dict(saved=None), dict(dx=None), dict(dga=None), dict(dgx=None), dict(ddecay=None), dict(dga=64),
+                   dict(dx=56), dict(ddecay=512)):
+        assert backward(**change) == INVALID, change
+    assert backward() == cb.CONV_ERR_WORKSPACE
+
+
+def adamw(lib, entries=None, count=None, pd=F, gd=F, bits=32, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, wd=0.0, step=1,
+          step_device=None, scale=None):
+    rows = entries if entries is not None else [dict()]
+    table = (optimizer.AdamWTensor * max(1, len(rows)))()
+    for t, e in zip(table, rows):
+        e = dict(dict(param=4096, master=None, grad=64, exp_avg=128, exp_avg_sq=192, exp_avg_scale=None, exp_avg_sq_scale=None,
+                      numel=8), **e)
+        for k, v in e.items():
+            setattr(t, k, v)
+    return lib.adamw_step(table, len(rows) if count is None else count, pd, gd, bits, lr, b1, b2, eps, wd, step, step_device,
+                          scale, 0, None)
+
+
+@pytest.mark.parametrize("change, status", [
+    (dict(count=-1), INVALID), (dict(pd=4), INVALID), (dict(gd=-1), INVALID), (dict(bits=16), INVALID), (dict(lr=-1.0), INVALID),
+    (dict(lr=float("nan")), INVALID), (dict(b1=1.0), INVALID), (dict(b2=-0.1), INVALID), (dict(eps=float("inf")), INVALID),
+    (dict(wd=-1.0), INVALID), (dict(step=0), INVALID), (dict(entries=[dict(param=None)]), INVALID),
+    (dict(entries=[dict(grad=None)]), INVALID), (dict(entries=[dict(exp_avg=None)]), INVALID),
+    (dict(entries=[dict(exp_avg_sq=None)]), INVALID), (dict(entries=[dict(numel=-1)]), INVALID),
+    (dict(bits=8), INVALID), (dict(entries=[dict(master=256)]), INVALID),
+    (dict(pd=BF, entries=[dict(master=256), dict(param=8192)]), INVALID),
+    (dict(entries=[dict(), dict()]), INVALID), (dict(entries=[dict(), dict(param=4112)]), INVALID),
+    (dict(entries=[dict(param=4100)]), UNSUPPORTED), (dict(entries=[dict(grad=72)]), UNSUPPORTED),
+    (dict(entries=[dict(numel=2 ** 41 + 1)]), UNSUPPORTED), (dict(step_device=4), UNSUPPORTED), (dict(scale=2), UNSUPPORTED),
+], ids=str)
+def test_adamw_refusals(lib, change, status):
+    assert adamw(lib, **change) == status
+    assert cb.conv2d_last_error()
+
+
+def test_layers_refuse_on_the_host(lib):
+    w = torch.zeros(6, 4)
+    for bad in (lambda: cb.CausalConv1dB200(torch.zeros(6)), lambda: cb.CausalConv1dB200(torch.zeros(6, 1)),
+                lambda: cb.CausalConv1dB200(torch.zeros(6, 9)), lambda: cb.CausalConv1dB200(w, activation="relu"),
+                lambda: cb.CausalConv1dB200(w, torch.zeros(5)), lambda: cb.CausalConv1dB200(torch.zeros(4, 6).t()),
+                lambda: cb.GatedRecurrenceB200(torch.zeros(2, 3))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: cb.CausalConv1dB200(w.half()), lambda: cb.CausalConv1dB200(w, torch.zeros(6).bfloat16()),
+                lambda: cb.GatedRecurrenceB200(torch.zeros(3).bfloat16())):
+        with pytest.raises(TypeError):
+            bad()
+    conv, rec = cb.CausalConv1dB200(w), cb.GatedRecurrenceB200(torch.zeros(6))
+    x = torch.zeros(2, 3, 6)
+    for bad in (lambda: conv(x), lambda: conv(torch.zeros(2, 3, 5)), lambda: rec(x, x, x), lambda: conv.step(x, x),
+                lambda: cb.AdamWB200([w]), lambda: cb.AdamWB200([])):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        conv(x.bfloat16())
+
+
+def test_reference_gradients_against_differences():
+    """The 64-bit reference's own gradients, against central differences of its loss."""
+    gen = torch.Generator().manual_seed(3)
+    normal = lambda *s: torch.randn(*s, generator=gen, dtype=torch.float64)  # noqa: E731
+    seqs, C, K = [(0, 3), (3, 0), (3, 5)], 2, 3
+    x, ga, gx, decay, h0 = normal(8, C), normal(8, C), normal(8, C), normal(C), normal(3, C)
+    w, b, s0 = normal(C, K), normal(C), normal(3, K - 1, C)
+    cy, cf, hy, hf = normal(8, C), normal(3, K - 1, C), normal(8, C), normal(3, C)
+
+    def conv_loss(x, w, b, s0):
+        y, final, _ = ref.conv1d(x, w, b, True, seqs, s0)
+        return (y * cy).sum() + (final * cf).sum()
+
+    def rec_loss(x, ga, gx, decay, h0):
+        h, final, _ = ref.recurrence(x, ga, gx, decay, 8.0, seqs, h0)
+        return (h * hy).sum() + (final * hf).sum()
+
+    for loss, args in ((conv_loss, (x, w, b, s0)), (rec_loss, (x, ga, gx, decay, h0))):
+        args = [a.clone().requires_grad_() for a in args]
+        grads = torch.autograd.grad(loss(*args), args)
+        for i, g in enumerate(grads):
+            d = normal(*g.shape)
+            at = lambda e: loss(*[a.detach() + (e * d if j == i else 0) for j, a in enumerate(args)])  # noqa: E731, B023
+            # the difference is off by eps^2 times a third derivative of order 100, and 1e-15/eps
+            assert abs((at(1e-5) - at(-1e-5)) / 2e-5 - (g * d).sum()) <= 1e-7 * (1 + g.abs().sum())
