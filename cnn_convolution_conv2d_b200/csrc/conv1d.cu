@@ -6,7 +6,11 @@
 // All three are bound by HBM: 2K + ~10 operations for 4 to 8 bytes.  A warp takes a strip of
 // rows of 32*V channels and slides down it with the last K-1 rows in registers, so each row
 // is read once (plus K-1 rows in front of a strip, which the neighbouring warp brings into L2).
-// Rows are loaded U at a time ahead of the arithmetic to keep enough bytes in flight.
+// Rows travel ahead of their use in a ring in shared memory, in which every thread copies and
+// reads its own places only: no barriers, and no registers or load counters held meanwhile (with
+// prefetched rows in registers a warp waited for its newest load at every row, 2.4 times slower,
+// or spilled).
+#include "ptx.cuh"
 #include "sequence.cuh"
 
 namespace conv2d_b200 {
@@ -27,7 +31,7 @@ struct Chan {
     __device__ bool any() const { return c < C; }
 };
 
-template <typename T, int V> struct Raw { T v[V]; };
+template <typename T, int V> struct alignas(sizeof(T) * V) Raw { T v[V]; };
 
 template <typename T, int V, bool kVec>
 __device__ __forceinline__ Raw<T, V> load_raw(const T *row, const Chan<T, V, kVec> &ch) {
@@ -44,18 +48,101 @@ __device__ __forceinline__ Raw<T, V> load_raw(const T *row, const Chan<T, V, kVe
     return r;
 }
 
+// Copies a lane's channels of a row to its place in the ring, asynchronously where the copy
+// instruction has the size (4 bytes and more).
 template <typename T, int V, bool kVec>
-__device__ __forceinline__ void load(float (&f)[V], const T *row, const Chan<T, V, kVec> &ch) {
-    const Raw<T, V> r = load_raw<T, V, kVec>(row, ch);
+__device__ __forceinline__ void copy_ahead(Raw<T, V> *to, const T *row, const Chan<T, V, kVec> &ch) {
+    if constexpr (kVec) {
+        if (ch.any()) ptx::cp_async<sizeof(Raw<T, V>)>(to, row + ch.c);
+    } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = to_float(r.v[v]);
+        for (int v = 0; v < V; ++v)
+            if (ch.has(v)) ptx::cp_async<4>(&to->v[v], row + ch.at(v));
+    } else {
+        *to = load_raw<T, V, kVec>(row, ch);
+    }
+}
+
+constexpr int kRing = 3;  // batches in the ring: one at work, two on their way
+
+// V channels as pairs: the arithmetic runs two channels to an instruction.
+template <int V> struct Pairs { float2 p[V / 2]; };
+
+template <int V>
+__device__ __forceinline__ Pairs<V> zero_pairs() {
+    Pairs<V> r;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) r.p[i] = make_float2(0.f, 0.f);
+    return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ Pairs<V> pairs(const Raw<T, V> &raw) {
+    Pairs<V> r;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) r.p[i] = make_float2(to_float(raw.v[2 * i]), to_float(raw.v[2 * i + 1]));
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Pairs<V> pairs(const float (&f)[V]) {
+    Pairs<V> r;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) r.p[i] = make_float2(f[2 * i], f[2 * i + 1]);
+    return r;
+}
+template <int V>
+__device__ __forceinline__ void add_product(Pairs<V> &sum, const Pairs<V> &a, const Pairs<V> &b) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) sum.p[i] = __ffma2_rn(a.p[i], b.p[i], sum.p[i]);
+}
+template <int V>
+__device__ __forceinline__ Pairs<V> sigmoid(const Pairs<V> &z) {
+    Pairs<V> r;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+        const float2 t = __fmul2_rn(z.p[i], make_float2(-kLog2e, -kLog2e));
+        const float2 d = __fadd2_rn(make_float2(ex2_approx(t.x), ex2_approx(t.y)), make_float2(1.f, 1.f));
+        r.p[i] = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+    }
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Pairs<V> mul(const Pairs<V> &a, const Pairs<V> &b) {
+    Pairs<V> r;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) r.p[i] = __fmul2_rn(a.p[i], b.p[i]);
+    return r;
+}
+// The derivative of z sigmoid(z) is s (1 + z (1 - s)) with s = sigmoid(z).
+template <int V>
+__device__ __forceinline__ Pairs<V> silu_slope(const Pairs<V> &z) {
+    const Pairs<V> s = sigmoid<V>(z);
+    Pairs<V> r;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+        const float2 one = make_float2(1.f, 1.f);
+        const float2 rest = __ffma2_rn(s.p[i], make_float2(-1.f, -1.f), one);
+        r.p[i] = __fmul2_rn(s.p[i], __ffma2_rn(z.p[i], rest, one));
+    }
+    return r;
 }
 
 template <typename T, int V, bool kVec>
-__device__ __forceinline__ void store(T *row, const float (&f)[V], const Chan<T, V, kVec> &ch) {
+__device__ __forceinline__ Pairs<V> load(const T *row, const Chan<T, V, kVec> &ch) {
+    return pairs<T, V>(load_raw<T, V, kVec>(row, ch));
+}
+
+template <typename T, int V, bool kVec>
+__device__ __forceinline__ void store(T *row, const Pairs<V> &f, const Chan<T, V, kVec> &ch) {
     Raw<T, V> r;
 #pragma unroll
-    for (int v = 0; v < V; ++v) r.v[v] = from_float<T>(f[v]);
+    for (int i = 0; i < V / 2; ++i) {
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<__nv_bfloat162 *>(&r.v[2 * i]) = __float22bfloat162_rn(f.p[i]);
+        } else {
+            r.v[2 * i] = f.p[i].x;
+            r.v[2 * i + 1] = f.p[i].y;
+        }
+    }
     if constexpr (kVec) {
         if (ch.any()) {
             if constexpr (sizeof(r) == 16) *reinterpret_cast<uint4 *>(row + ch.c) = *reinterpret_cast<uint4 *>(&r);
@@ -70,28 +157,26 @@ __device__ __forceinline__ void store(T *row, const float (&f)[V], const Chan<T,
 }
 
 template <typename T, int K, int V, bool kVec>
-__device__ __forceinline__ void load_weights(float (&w)[K][V], float (&b)[V], const void *wp, const void *bp,
+__device__ __forceinline__ void load_weights(Pairs<V> (&w)[K], Pairs<V> &b, const void *wp, const void *bp,
                                              const Chan<T, V, kVec> &ch) {
     const T *wt = static_cast<const T *>(wp), *bt = static_cast<const T *>(bp);
+    float f[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const bool has = ch.has(v);
-        b[v] = has && bt ? to_float(bt[ch.at(v)]) : 0.f;
+    for (int v = 0; v < V; ++v) f[v] = ch.has(v) && bt ? to_float(bt[ch.at(v)]) : 0.f;
+    b = pairs<V>(f);
 #pragma unroll
-        for (int k = 0; k < K; ++k) w[k][v] = has ? to_float(wt[static_cast<size_t>(ch.at(v)) * K + k]) : 0.f;
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[v] = ch.has(v) ? to_float(wt[static_cast<size_t>(ch.at(v)) * K + k]) : 0.f;
+        w[k] = pairs<V>(f);
     }
 }
 
 // Row `before` rows ahead of a sequence's first one (1 <= before <= K-1).
 template <typename T, int K, int V, bool kVec>
-__device__ __forceinline__ void load_state(float (&f)[V], const void *state, int s, int before,
-                                           const Chan<T, V, kVec> &ch) {
-    if (state) {
-        load<T, V, kVec>(f, static_cast<const T *>(state) + (static_cast<size_t>(s) * (K - 1) + (K - 1 - before)) * ch.C, ch);
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) f[v] = 0.f;
-    }
+__device__ __forceinline__ Pairs<V> load_state(const void *state, int s, int before, const Chan<T, V, kVec> &ch) {
+    if (!state) return zero_pairs<V>();
+    return load<T, V, kVec>(static_cast<const T *>(state) + (static_cast<size_t>(s) * (K - 1) + (K - 1 - before)) * ch.C, ch);
 }
 
 // Where a strip stands among the sequences.
@@ -128,22 +213,44 @@ struct Cursor {
     __device__ bool inside(const Sequences &q) const { return s >= 0 && s < q.nseq; }
 };
 
+// The K-1 rows in front of row `row`: of its sequence, or of the window ahead of it.
+template <typename T, int K, int V, bool kVec>
+__device__ __forceinline__ void load_window(Pairs<V> (&win)[K - 1], const Conv1dParams &p, const Cursor &cur, int row,
+                                            const Chan<T, V, kVec> &ch) {
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+        const int back = K - 1 - j;
+        if (!cur.inside(p.seq)) win[j] = zero_pairs<V>();
+        else if (row - back >= cur.begin)
+            win[j] = load<T, V, kVec>(static_cast<const T *>(p.x) + static_cast<size_t>(row - back) * p.ldx, ch);
+        else win[j] = load_state<T, K, V, kVec>(p.state, cur.s, back - (row - cur.begin), ch);
+    }
+}
+
 // final_state[s]: the last K-1 rows of (window, x).  One block of the grid for a tile and a sequence.
 template <typename T, int K, int V, bool kVec>
 __device__ __forceinline__ void copy_final(const Conv1dParams &p, int s, const Chan<T, V, kVec> &ch) {
     const int begin = seq_begin(p.seq, s), n = max(0, seq_begin(p.seq, s + 1) - begin);
     for (int j = threadIdx.x >> 5; j < K - 1; j += kConvWarps) {
         const int place = n - (K - 1) + j;
-        float f[V];
-        if (place >= 0) load<T, V, kVec>(f, static_cast<const T *>(p.x) + static_cast<size_t>(begin + place) * p.ldx, ch);
-        else load_state<T, K, V, kVec>(f, p.state, s, -place, ch);
+        const Pairs<V> f = place >= 0
+                               ? load<T, V, kVec>(static_cast<const T *>(p.x) + static_cast<size_t>(begin + place) * p.ldx, ch)
+                               : load_state<T, K, V, kVec>(p.state, s, -place, ch);
         store<T, V, kVec>(static_cast<T *>(p.final_state) + (static_cast<size_t>(s) * (K - 1) + j) * p.C, f, ch);
     }
 }
 
+// Moves a window of rows on by one.
+template <int N, int V>
+__device__ __forceinline__ void shift_in(Pairs<V> (&win)[N], const Pairs<V> &row) {
+#pragma unroll
+    for (int j = 0; j + 1 < N; ++j) win[j] = win[j + 1];
+    win[N - 1] = row;
+}
+
 template <typename T, int K, int V, bool kVec>
-__global__ void __launch_bounds__(kConvWarps * 32) conv1d_forward_kernel(Conv1dParams p) {
-    constexpr int U = 8;
+__global__ void __launch_bounds__(kConvWarps * 32, 6) conv1d_forward_kernel(const __grid_constant__ Conv1dParams p) {
+    constexpr int U = 8 * 2 / sizeof(T);
     const int tile = blockIdx.x % p.tiles, block = blockIdx.x / p.tiles;  // neighbours share rows
     const Chan<T, V, kVec> ch(tile, p.C);
     if (blockIdx.x == 0) check_offsets(p.seq, p.status);
@@ -154,72 +261,73 @@ __global__ void __launch_bounds__(kConvWarps * 32) conv1d_forward_kernel(Conv1dP
     const long long first = (static_cast<long long>(block) * kConvWarps + (threadIdx.x >> 5)) * p.strip;
     if (first >= p.seq.rows) return;
     const int row0 = static_cast<int>(first), row1 = min(p.seq.rows - row0, p.strip) + row0;
-    const T *x = static_cast<const T *>(p.x);
-    T *y = static_cast<T *>(p.y);
-    float w[K][V], b[V], win[K - 1][V];
+    const T *x = static_cast<const T *>(p.x) + static_cast<size_t>(row0) * p.ldx;
+    T *y = static_cast<T *>(p.y) + static_cast<size_t>(row0) * p.ldy;
+    __shared__ Raw<T, V> s_ring[kRing][U][kConvWarps * 32];
+    auto fetch = [&](int row, const T *from, int slot) {  // the batch of rows from `row` on
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (row + u < row1) copy_ahead<T, V, kVec>(&s_ring[slot][u][threadIdx.x], from + u * p.ldx, ch);
+        ptx::cp_async_commit();
+    };
+    fetch(row0, x, 0);
+    fetch(row0 + U, x + U * p.ldx, 1);
+    Pairs<V> w[K], b, win[K - 1];
     load_weights<T, K, V, kVec>(w, b, p.w, p.bias, ch);
     Cursor cur;
     cur.place(p.seq, row0);
+    load_window<T, K, V, kVec>(win, p, cur, row0, ch);
+    auto result = [&](const Pairs<V> *rows) {  // from the K rows that end with the result's own
+        Pairs<V> z = b;
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) {  // win[j]: row row0 - (K-1) + j
-        const int back = K - 1 - j;
-#pragma unroll
-        for (int v = 0; v < V; ++v) win[j][v] = 0.f;
-        if (cur.inside(p.seq)) {
-            if (row0 - back >= cur.begin) load<T, V, kVec>(win[j], x + static_cast<size_t>(row0 - back) * p.ldx, ch);
-            else load_state<T, K, V, kVec>(win[j], p.state, cur.s, back - (row0 - cur.begin), ch);
-        }
-    }
+        for (int k = 0; k < K; ++k) add_product<V>(z, w[k], rows[k]);
+        return p.silu ? mul<V>(z, sigmoid<V>(z)) : z;
+    };
+    int slot = 0;
     for (int row = row0; row < row1; row += U) {
-        Raw<T, V> raw[U];
+        fetch(row + 2 * U, x + 2 * U * p.ldx, slot ? slot - 1 : kRing - 1);
+        ptx::cp_async_wait<kRing - 1>();
+        if (cur.inside(p.seq) && row + U <= min(cur.end, row1)) {
+            Pairs<V> all[K - 1 + U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (row + u < row1) raw[u] = load_raw<T, V, kVec>(x + static_cast<size_t>(row + u) * p.ldx, ch);
+            for (int j = 0; j < K - 1; ++j) all[j] = win[j];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (row + u >= row1) break;
-            if (row + u >= cur.end) {
-                cur.next(p.seq, row + u);
-                if (cur.inside(p.seq)) {
+            for (int u = 0; u < U; ++u) {
+                all[K - 1 + u] = pairs<T, V>(s_ring[slot][u][threadIdx.x]);
+                store<T, V, kVec>(y + u * p.ldy, result(all + u), ch);
+            }
 #pragma unroll
-                    for (int j = 0; j < K - 1; ++j) load_state<T, K, V, kVec>(win[j], p.state, cur.s, K - 1 - j, ch);
+            for (int j = 0; j < K - 1; ++j) win[j] = all[U + j];
+        } else {  // a sequence or the strip ends here: row by row
+#pragma unroll 1
+            for (int u = 0; u < U && row + u < row1; ++u) {
+                if (row + u >= cur.end) {
+                    cur.next(p.seq, row + u);
+                    load_window<T, K, V, kVec>(win, p, cur, row + u, ch);
                 }
+                Pairs<V> all[K];
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j) all[j] = win[j];
+                all[K - 1] = pairs<T, V>(s_ring[slot][u][threadIdx.x]);
+                if (cur.inside(p.seq)) store<T, V, kVec>(y + u * p.ldy, result(all), ch);
+                shift_in<K - 1, V>(win, all[K - 1]);
             }
-            float z[V], xv[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                xv[v] = to_float(raw[u].v[v]);
-                z[v] = b[v];
-            }
-#pragma unroll
-            for (int k = 0; k < K - 1; ++k)
-#pragma unroll
-                for (int v = 0; v < V; ++v) z[v] = fmaf(w[k][v], win[k][v], z[v]);
-#pragma unroll
-            for (int v = 0; v < V; ++v) z[v] = fmaf(w[K - 1][v], xv[v], z[v]);
-            if (p.silu) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) z[v] *= sigmoid(z[v]);
-            }
-            if (cur.inside(p.seq)) store<T, V, kVec>(y + static_cast<size_t>(row + u) * p.ldy, z, ch);
-#pragma unroll
-            for (int j = 0; j + 1 < K - 1; ++j)
-#pragma unroll
-                for (int v = 0; v < V; ++v) win[j][v] = win[j + 1][v];
-#pragma unroll
-            for (int v = 0; v < V; ++v) win[K - 2][v] = xv[v];
         }
+        slot = slot == kRing - 1 ? 0 : slot + 1;
+        x += U * p.ldx;
+        y += U * p.ldy;
     }
 }
 
-// Backward.  Going down the rows, row t's dz completes the gradient of row t-(K-1), so the last
-// K-1 dz's wait in registers as partly summed gradients: dxp[j] is the sum so far for the row
-// K-1-j rows back (a row ahead of the sequence is a row of the carried window).  K-1 rows behind
-// the strip are read for the dz's that its last rows still need.
+// Backward.  Going down the rows, row t's dz completes the gradient of row t-(K-1):
+// dx[t-(K-1)] = sum_j w[K-1-j] dz[t-(K-1)+j], from the last K-1 dz's in registers (zeros ahead of the
+// sequence; a target ahead of the sequence is a row of the carried window).  K-1 rows behind the strip
+// are read for the dz's that its last rows still need.
 template <typename T, int K, int V, bool kVec>
-__global__ void __launch_bounds__(kConvWarps * 32) conv1d_backward_kernel(Conv1dParams p) {
-    constexpr int U = 4;
-    __shared__ float s_sum[kConvWarps][32 * V];
+__global__ void __launch_bounds__(kConvWarps * 32, 4) conv1d_backward_kernel(const __grid_constant__ Conv1dParams p) {
+    constexpr int U = 4 * 2 / sizeof(T);
+    __shared__ float2 s_sum[kConvWarps][16 * V];
+    __shared__ Raw<T, V> s_ring[kRing][2][U][kConvWarps * 32];
     const int tile = blockIdx.x % p.tiles, block = blockIdx.x / p.tiles;  // neighbours share rows
     const Chan<T, V, kVec> ch(tile, p.C);
     if (blockIdx.x == 0) check_offsets(p.seq, p.status);
@@ -227,157 +335,162 @@ __global__ void __launch_bounds__(kConvWarps * 32) conv1d_backward_kernel(Conv1d
     if (block >= p.row_blocks) {  // d_state of an empty sequence: d_final itself
         const int s = block - p.row_blocks;
         if (seq_begin(p.seq, s + 1) > seq_begin(p.seq, s)) return;
-        for (int j = warp; j < K - 1; j += kConvWarps) {
-            float f[V];
-            load_state<T, K, V, kVec>(f, p.d_final, s, K - 1 - j, ch);
-            store<T, V, kVec>(static_cast<T *>(p.d_state) + (static_cast<size_t>(s) * (K - 1) + j) * p.C, f, ch);
-        }
+        for (int j = warp; j < K - 1; j += kConvWarps)
+            store<T, V, kVec>(static_cast<T *>(p.d_state) + (static_cast<size_t>(s) * (K - 1) + j) * p.C,
+                              load_state<T, K, V, kVec>(p.d_final, s, K - 1 - j, ch), ch);
         return;
     }
-    const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy);
-    T *dx = static_cast<T *>(p.y);
-    float w[K][V], b[V], dw[K][V], db[V];
+    Pairs<V> w[K], b, dw[K], db = zero_pairs<V>();
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        db[v] = 0.f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) dw[k][v] = 0.f;
-    }
+    for (int k = 0; k < K; ++k) dw[k] = zero_pairs<V>();
     const long long first = (static_cast<long long>(block) * kConvWarps + warp) * p.strip;
     if (first < p.seq.rows) {
         const int row0 = static_cast<int>(first), row1 = min(p.seq.rows - row0, p.strip) + row0;
         const int last = min(p.seq.rows - row1, K - 1) + row1;  // rows read
-        load_weights<T, K, V, kVec>(w, b, p.w, p.bias, ch);
-        float win[K - 1][V], dxp[K][V];
-        Cursor cur;
-        cur.place(p.seq, row0);
-#pragma unroll
-        for (int j = 0; j < K; ++j)
-#pragma unroll
-            for (int v = 0; v < V; ++v) dxp[j][v] = 0.f;
-#pragma unroll
-        for (int j = 0; j < K - 1; ++j) {
-            const int back = K - 1 - j;
-#pragma unroll
-            for (int v = 0; v < V; ++v) win[j][v] = 0.f;
-            if (cur.inside(p.seq)) {
-                if (row0 - back >= cur.begin) load<T, V, kVec>(win[j], x + static_cast<size_t>(row0 - back) * p.ldx, ch);
-                else load_state<T, K, V, kVec>(win[j], p.state, cur.s, back - (row0 - cur.begin), ch);
-            }
-        }
-        // Writes the finished gradient of the row K-1 rows ahead of `t` of sequence `cur`.
-        auto emit = [&](int t) {
-            const int target = t - (K - 1);
-            if (target >= cur.begin) {
-                if (target >= row0 && target < row1) store<T, V, kVec>(dx + static_cast<size_t>(target) * p.ldy, dxp[0], ch);
-            } else if (p.d_state && cur.begin >= row0 && cur.begin < row1) {
-                store<T, V, kVec>(static_cast<T *>(p.d_state) +
-                                      (static_cast<size_t>(cur.s) * (K - 1) + (target - cur.begin + K - 1)) * p.C,
-                                  dxp[0], ch);
-            }
-#pragma unroll
-            for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-                for (int v = 0; v < V; ++v) dxp[j][v] = dxp[j + 1][v];
-#pragma unroll
-            for (int v = 0; v < V; ++v) dxp[K - 1][v] = 0.f;
-        };
-        // Behind a sequence's last row: its last K-1 rows (and d_final) are finished.
-        auto flush = [&](int end) {
-#pragma unroll
-            for (int j = 0; j < K - 1; ++j) {
-                if (p.d_final) {
-                    float f[V];
-                    load_state<T, K, V, kVec>(f, p.d_final, cur.s, K - 1 - j, ch);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) dxp[0][v] += f[v];
-                }
-                emit(end + j);
-            }
-        };
-        bool done = false;
-        for (int row = row0; row < last && !done; row += U) {
-            Raw<T, V> rx[U], rd[U];
+        const T *x = static_cast<const T *>(p.x) + static_cast<size_t>(row0) * p.ldx;
+        const T *dy = static_cast<const T *>(p.dy) + static_cast<size_t>(row0) * p.lddy;
+        T *dx = static_cast<T *>(p.y);
+        auto fetch = [&](int row, const T *from_x, const T *from_d, int slot) {  // the batch of rows from `row` on
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (row + u < last) {
-                    rx[u] = load_raw<T, V, kVec>(x + static_cast<size_t>(row + u) * p.ldx, ch);
-                    rd[u] = load_raw<T, V, kVec>(dy + static_cast<size_t>(row + u) * p.lddy, ch);
+                    copy_ahead<T, V, kVec>(&s_ring[slot][0][u][threadIdx.x], from_x + u * p.ldx, ch);
+                    copy_ahead<T, V, kVec>(&s_ring[slot][1][u][threadIdx.x], from_d + u * p.lddy, ch);
                 }
+            ptx::cp_async_commit();
+        };
+        fetch(row0, x, dy, 0);
+        fetch(row0 + U, x + U * p.ldx, dy + U * p.lddy, 1);
+        load_weights<T, K, V, kVec>(w, b, p.w, p.bias, ch);
+        Pairs<V> win[K - 1], past[K - 1];  // x and dz of the K-1 rows before
+        Cursor cur;
+        cur.place(p.seq, row0);
+        load_window<T, K, V, kVec>(win, p, cur, row0, ch);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int t = row + u;
-                if (t >= last || done) break;
-                if (t >= cur.end) {
-                    if (cur.inside(p.seq)) flush(cur.end);
-                    if (t >= row1) {  // what follows the strip's last sequence is none of the strip's
-                        done = true;
-                        break;
-                    }
-                    cur.next(p.seq, t);
-                    if (cur.inside(p.seq)) {
+        for (int j = 0; j < K - 1; ++j) past[j] = zero_pairs<V>();
+        // dz of a row from its dy, and the K rows of x that end with it
+        auto slope = [&](const Pairs<V> &d, const Pairs<V> *rows) {
+            if (!p.silu) return d;
+            Pairs<V> z = b;
 #pragma unroll
-                        for (int j = 0; j < K - 1; ++j) load_state<T, K, V, kVec>(win[j], p.state, cur.s, K - 1 - j, ch);
-                    }
-                }
-                if (!cur.inside(p.seq)) {
-                    if (t >= row1) done = true;
-                    continue;
-                }
-                float xv[V], dz[V];
+            for (int k = 0; k < K; ++k) add_product<V>(z, w[k], rows[k]);
+            return mul<V>(d, silu_slope<V>(z));
+        };
+        auto sums = [&](const Pairs<V> &d, const Pairs<V> *rows) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    xv[v] = to_float(rx[u].v[v]);
-                    dz[v] = to_float(rd[u].v[v]);
-                }
-                if (p.silu) {
+            for (int i = 0; i < V / 2; ++i) db.p[i] = __fadd2_rn(db.p[i], d.p[i]);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        float z = b[v];
+            for (int k = 0; k < K; ++k) add_product<V>(dw[k], d, rows[k]);
+        };
+        auto gradient = [&](const Pairs<V> *dz) {  // of the first of K rows, from their dz
+            Pairs<V> g = mul<V>(w[K - 1], dz[0]);
 #pragma unroll
-                        for (int k = 0; k < K - 1; ++k) z = fmaf(w[k][v], win[k][v], z);
-                        z = fmaf(w[K - 1][v], xv[v], z);
-                        const float sg = sigmoid(z);
-                        dz[v] *= sg * fmaf(z, 1.f - sg, 1.f);
-                    }
-                }
-                if (t < row1) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        db[v] += dz[v];
-#pragma unroll
-                        for (int k = 0; k < K - 1; ++k) dw[k][v] = fmaf(dz[v], win[k][v], dw[k][v]);
-                        dw[K - 1][v] = fmaf(dz[v], xv[v], dw[K - 1][v]);
-                    }
-                }
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-#pragma unroll
-                    for (int k = 0; k < K; ++k) dxp[k][v] = fmaf(w[k][v], dz[v], dxp[k][v]);
-#pragma unroll
-                    for (int j = 0; j + 1 < K - 1; ++j) win[j][v] = win[j + 1][v];
-                    win[K - 2][v] = xv[v];
-                }
-                emit(t);
+            for (int j = 1; j < K; ++j) add_product<V>(g, w[K - 1 - j], dz[j]);
+            return g;
+        };
+        // The gradient of the row K-1 rows ahead of row t of sequence `cur`, to where it belongs.
+        auto emit = [&](int t, const Pairs<V> &g) {
+            const int target = t - (K - 1);
+            if (target >= cur.begin) {
+                if (target >= row0 && target < row1) store<T, V, kVec>(dx + static_cast<size_t>(target) * p.ldy, g, ch);
+            } else if (p.d_state && cur.begin >= row0 && cur.begin < row1) {
+                store<T, V, kVec>(static_cast<T *>(p.d_state) +
+                                      (static_cast<size_t>(cur.s) * (K - 1) + (target - cur.begin + K - 1)) * p.C, g, ch);
             }
+        };
+        // Behind a sequence's last row: its last K-1 rows, with what d_final sends them, are finished.
+        auto flush = [&]() {
+#pragma unroll 1
+            for (int i = 0; i < K - 1; ++i) {
+                Pairs<V> g = load_state<T, K, V, kVec>(p.d_final, cur.s, K - 1 - i, ch);
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j) add_product<V>(g, w[K - 1 - j], past[j]);
+                emit(cur.end + i, g);
+                shift_in<K - 1, V>(past, zero_pairs<V>());
+            }
+        };
+        bool done = false;
+        int slot = 0;
+        for (int row = row0; row < last && !done; row += U) {
+            fetch(row + 2 * U, x + 2 * U * p.ldx, dy + 2 * U * p.lddy, slot ? slot - 1 : kRing - 1);
+            ptx::cp_async_wait<kRing - 1>();
+            if (cur.inside(p.seq) && row + U <= cur.end && row - (K - 1) >= cur.begin) {
+                Pairs<V> all[K - 1 + U], dz[K - 1 + U];
+                T *to = dx + static_cast<ptrdiff_t>(row - (K - 1)) * p.ldy;
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j) {
+                    all[j] = win[j];
+                    dz[j] = past[j];
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int t = row + u;
+                    all[K - 1 + u] = pairs<T, V>(s_ring[slot][0][u][threadIdx.x]);
+                    dz[K - 1 + u] = slope(pairs<T, V>(s_ring[slot][1][u][threadIdx.x]), all + u);
+                    if (t < row1) sums(dz[K - 1 + u], all + u);
+                    if (t - (K - 1) >= row0 && t - (K - 1) < row1)  // (rows behind `last` hold nothing, and end here)
+                        store<T, V, kVec>(to + u * p.ldy, gradient(dz + u), ch);
+                }
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j) {
+                    win[j] = all[U + j];
+                    past[j] = dz[U + j];
+                }
+            } else {  // a sequence begins or ends here: row by row
+#pragma unroll 1
+                for (int u = 0; u < U && row + u < last; ++u) {
+                    const int t = row + u;
+                    if (t >= cur.end) {
+                        if (cur.inside(p.seq)) flush();
+                        cur.next(p.seq, t);
+                        load_window<T, K, V, kVec>(win, p, cur, t, ch);
+                        // what follows the strip's last sequence is none of the strip's
+                        if (t >= row1) cur.outside(p.seq);
+                    }
+                    if (!cur.inside(p.seq)) {
+                        if (t >= row1) {
+                            done = true;
+                            break;
+                        }
+                        continue;
+                    }
+                    Pairs<V> all[K], dz[K];
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) {
+                        all[j] = win[j];
+                        dz[j] = past[j];
+                    }
+                    all[K - 1] = pairs<T, V>(s_ring[slot][0][u][threadIdx.x]);
+                    dz[K - 1] = slope(pairs<T, V>(s_ring[slot][1][u][threadIdx.x]), all);
+                    if (t < row1) sums(dz[K - 1], all);
+                    emit(t, gradient(dz));
+                    shift_in<K - 1, V>(win, all[K - 1]);
+                    shift_in<K - 1, V>(past, dz[K - 1]);
+                }
+            }
+            slot = slot == kRing - 1 ? 0 : slot + 1;
+            x += U * p.ldx;
+            dy += U * p.lddy;
         }
         // the rows ended with this sequence
-        if (!done && cur.inside(p.seq) && last >= cur.end) flush(cur.end);
+        if (!done && cur.inside(p.seq) && last >= cur.end) flush();
     }
     // The block's sums of dw and db: its warps' in order, so that equal inputs give equal bits.
 #pragma unroll
     for (int k = 0; k < K + 1; ++k) {
         __syncthreads();
 #pragma unroll
-        for (int v = 0; v < V; ++v) s_sum[warp][v * 32 + (threadIdx.x & 31)] = k < K ? dw[k < K ? k : 0][v] : db[v];
+        for (int i = 0; i < V / 2; ++i) s_sum[warp][i * 32 + (threadIdx.x & 31)] = k < K ? dw[k < K ? k : 0].p[i] : db.p[i];
         __syncthreads();
-        for (int i = threadIdx.x; i < 32 * V; i += kConvWarps * 32) {
-            const int v = i >> 5, lane = i & 31;
+        for (int i = threadIdx.x; i < 16 * V; i += kConvWarps * 32) {
+            const int v = i >> 5 << 1, lane = i & 31;
             const int c = tile * 32 * V + (kVec ? lane * V + v : lane + 32 * v);
-            float sum = 0.f;
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int q = 0; q < kConvWarps; ++q) sum += s_sum[q][i];
-            if (c < p.C) p.partial[(static_cast<size_t>(block) * (K + 1) + k) * p.C + c] = sum;
+            for (int q = 0; q < kConvWarps; ++q) sum = __fadd2_rn(sum, s_sum[q][i]);
+            float *out = p.partial + (static_cast<size_t>(block) * (K + 1) + k) * p.C;
+            if (c < p.C) out[c] = sum.x;
+            if (c + (kVec ? 1 : 32) < p.C) out[c + (kVec ? 1 : 32)] = sum.y;
         }
     }
 }
@@ -406,37 +519,29 @@ __global__ void __launch_bounds__(1024) conv1d_reduce_kernel(const float *partia
 }
 
 template <typename T, int K, int V, bool kVec>
-__global__ void __launch_bounds__(128) conv1d_step_kernel(Conv1dStepParams p) {
+__global__ void __launch_bounds__(128) conv1d_step_kernel(const __grid_constant__ Conv1dStepParams p) {
     const Chan<T, V, kVec> ch(blockIdx.x % p.tiles * 4 + (threadIdx.x >> 5), p.C);
     const int b = blockIdx.x / p.tiles;
     const int slot = p.slots ? p.slots[b] : b;
-    float w[K][V], bias[V], xv[V];
-    load<T, V, kVec>(xv, static_cast<const T *>(p.x) + static_cast<size_t>(b) * p.ldx, ch);
-    load_weights<T, K, V, kVec>(w, bias, p.w, p.bias, ch);
+    const Pairs<V> x = load<T, V, kVec>(static_cast<const T *>(p.x) + static_cast<size_t>(b) * p.ldx, ch);
+    Pairs<V> w[K], z, win[K - 1];
+    load_weights<T, K, V, kVec>(w, z, p.w, p.bias, ch);
     if (slot < 0 || slot >= p.pool) return;  // the whole block: b names no window
     T *state = static_cast<T *>(p.state) + static_cast<size_t>(slot) * (K - 1) * p.C;
-    float win[K - 1][V];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) load<T, V, kVec>(win[j], state + static_cast<size_t>(j) * p.C, ch);
+    for (int j = 0; j < K - 1; ++j) win[j] = load<T, V, kVec>(state + static_cast<size_t>(j) * p.C, ch);
     if (p.slots && slot_named_before(p.slots, b, slot)) {
         if (threadIdx.x == 0) atomicExch(p.status, kDevBadSlot);
         return;
     }
-    float z[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        z[v] = bias[v];
-#pragma unroll
-        for (int k = 0; k < K - 1; ++k) z[v] = fmaf(w[k][v], win[k][v], z[v]);
-        z[v] = fmaf(w[K - 1][v], xv[v], z[v]);
-        if (p.silu) z[v] *= sigmoid(z[v]);
-    }
+    for (int k = 0; k < K - 1; ++k) add_product<V>(z, w[k], win[k]);
+    add_product<V>(z, w[K - 1], x);
+    if (p.silu) z = mul<V>(z, sigmoid<V>(z));
     store<T, V, kVec>(static_cast<T *>(p.y) + static_cast<size_t>(b) * p.ldy, z, ch);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) {
-        if (j + 1 < K - 1) store<T, V, kVec>(state + static_cast<size_t>(j) * p.C, win[j + 1 < K - 1 ? j + 1 : 0], ch);
-        else store<T, V, kVec>(state + static_cast<size_t>(j) * p.C, xv, ch);
-    }
+    for (int j = 0; j + 1 < K - 1; ++j) store<T, V, kVec>(state + static_cast<size_t>(j) * p.C, win[j + 1], ch);
+    store<T, V, kVec>(state + static_cast<size_t>(K - 2) * p.C, x, ch);
 }
 
 // Channels of one lane: few enough that weights, window and gradient sums stay in registers.
@@ -445,16 +550,16 @@ constexpr int lane_channels(int K) { return K <= 4 ? 4 : 2; }
 template <typename T, bool kVec, int K>
 cudaError_t forward_k(const Conv1dParams &p, cudaStream_t s) {
     constexpr int V = lane_channels(K);
-    conv1d_forward_kernel<T, K, V, kVec>
-        <<<p.tiles * (p.row_blocks + (p.final_state ? p.seq.nseq : 0)), kConvWarps * 32, 0, s>>>(p);
+    const int grid = p.tiles * (p.row_blocks + (p.final_state ? p.seq.nseq : 0));
+    conv1d_forward_kernel<T, K, V, kVec><<<grid, kConvWarps * 32, 0, s>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T, bool kVec, int K>
 cudaError_t backward_k(const Conv1dParams &p, cudaStream_t s) {
     constexpr int V = lane_channels(K);
-    conv1d_backward_kernel<T, K, V, kVec>
-        <<<p.tiles * (p.row_blocks + (p.d_state ? p.seq.nseq : 0)), kConvWarps * 32, 0, s>>>(p);
+    const int grid = p.tiles * (p.row_blocks + (p.d_state ? p.seq.nseq : 0));
+    conv1d_backward_kernel<T, K, V, kVec><<<grid, kConvWarps * 32, 0, s>>>(p);
     return cudaGetLastError();
 }
 
