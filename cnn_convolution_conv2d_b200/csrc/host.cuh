@@ -19,4 +19,9 @@ struct AbiDevice {
 // The current device; fails on one that this library is not built for.
 int abi_device(AbiDevice *out);
 
+// A matrix of `rows` rows of `cols` elements (2 or 4 bytes), rows `row_bytes` apart, as a tiled
+// tensor map without swizzle; what lies outside reads as zero and is not written.
+int abi_tensor_map_2d(CUtensorMap *map, const void *p, int elt, long long cols, long long rows, long long row_bytes,
+                      int box_cols, int box_rows);
+
 }  // namespace conv2d_b200

@@ -7,9 +7,11 @@
 // of its a's and H its result from a zero state, and two runs join by
 // (A1, H1), (A2, H2) -> (A1 A2, A2 H1 + H2): so the time axis is split.
 //
-// One work item is kRecChunk rows of kRecTile channels.  Its warps take equal runs of rows, a
-// lane two channels; each scans its run from zero in registers, the runs' (A, H) meet in shared
-// memory, and once the state in front of the item is known each warp scans again and writes.
+// One work item is a chunk of rows of kRecTile channels.  Its working warps take runs of rows, a lane two
+// channels; each scans its run from zero in registers and leaves the run's (A, H) in shared memory.  A
+// joining warp joins them, finds the state that enters the chunk, and hands every warp the state
+// that enters its run; then the warps write their results.  Two blocks an SM, so that one works
+// while the other's runs are joined.
 // Items are handed out by a counter, early rows first, so an item only waits for items that are
 // already running.  An item publishes its (A, H) as soon as it has them and the state behind
 // it as soon as it knows the one before; the next item takes the nearest published state and
@@ -19,6 +21,15 @@
 //
 // Sequence starts inside an item are cuts: there A = 0, and joining selects instead of
 // multiplying, so what a sequence holds (infinities and NaN too) never reaches its neighbour.
+//
+// Bound by HBM (8 bytes an element forward, 14 backward in bf16) with the arithmetic close
+// behind: two sigmoids, an exponential and a square root an element.  Hence two channels to an
+// instruction, and rows that travel by TMA, the next items' tiles while an item is at work, and
+// back from the same places in shared memory: with loads and stores of its own each thread spent
+// more on addresses than on the recurrence.  Tensors whose base or row stride is no multiple of
+// 16 bytes take the same item code with loads and stores of single elements.
+#include <atomic>
+
 #include "ptx.cuh"
 #include "sequence.cuh"
 
@@ -26,96 +37,154 @@ namespace conv2d_b200 {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kMaxKnown = 64;  // devices whose launch shapes are remembered
 
+// Two channels to an instruction.  (A product that a sum takes up right away is written as fma2: the
+// compiler fuses the two in some kernels and not in others, and results should not depend on that.)
+__device__ __forceinline__ uint64_t pair(float2 v) { return static_cast<uint64_t>(__float_as_uint(v.y)) << 32 | __float_as_uint(v.x); }
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+}
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair(a)), "l"(pair(b)));
+    return unpair(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair(a)), "l"(pair(b)));
+    return unpair(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair(a)), "l"(pair(b)), "l"(pair(c)));
+    return unpair(d);
+}
+__device__ __forceinline__ float2 add1(float2 a, float c) { return add2(a, splat(c)); }
+__device__ __forceinline__ float2 one_minus(float2 a) { return fma2(a, splat(-1.f), splat(1.f)); }
+__device__ __forceinline__ float2 negative(float2 a) { return make_float2(-a.x, -a.y); }
 
 // ----------------------------------------------------------- element access ---
-// The two channels of a lane: adjacent (kVec: one load; even C, strides and base), or 32 apart.
-template <typename T, bool kVec>
+// The two channels of a lane: adjacent, or 32 apart.
+template <bool kAdjacent>
 struct Lane2 {
     int c0, c1;
     bool ok0, ok1;
     __device__ Lane2(int tile, int C) {
         const int lane = threadIdx.x & 31;
-        c0 = tile * kRecTile + (kVec ? 2 * lane : lane);
-        c1 = c0 + (kVec ? 1 : 32);
+        c0 = tile * kRecTile + (kAdjacent ? 2 * lane : lane);
+        c1 = c0 + (kAdjacent ? 1 : 32);
         ok0 = c0 < C;
         ok1 = c1 < C;
     }
 };
 
-template <typename T> struct Raw2;
-template <> struct Raw2<float> {
-    float2 v;
-    __device__ float2 get() const { return v; }
-};
-template <> struct Raw2<__nv_bfloat16> {
-    uint32_t v;
-    __device__ float2 get() const { return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); }
-};
+template <typename T, bool kAdjacent>
+__device__ __forceinline__ float2 load2(const T *row, const Lane2<kAdjacent> &l) {
+    return make_float2(l.ok0 ? to_float(row[l.c0]) : 0.f, l.ok1 ? to_float(row[l.c1]) : 0.f);
+}
+template <typename T, bool kAdjacent>
+__device__ __forceinline__ void store2(T *row, float2 f, const Lane2<kAdjacent> &l) {
+    if (l.ok0) row[l.c0] = from_float<T>(f.x);
+    if (l.ok1) row[l.c1] = from_float<T>(f.y);
+}
+template <bool kAdjacent>
+__device__ __forceinline__ float2 load_f32(const float *row, const Lane2<kAdjacent> &l) {
+    return row ? load2<float>(row, l) : make_float2(0.f, 0.f);
+}
 
-template <typename T, bool kVec>
-__device__ __forceinline__ Raw2<T> load2(const T *row, const Lane2<T, kVec> &l) {
-    Raw2<T> r;
-    if constexpr (sizeof(T) == 4) {
-        if constexpr (kVec) {
-            r.v = l.ok0 ? __ldcs(reinterpret_cast<const float2 *>(row + l.c0)) : make_float2(0.f, 0.f);
-        } else {
-            r.v.x = l.ok0 ? __ldcs(row + l.c0) : 0.f;
-            r.v.y = l.ok1 ? __ldcs(row + l.c1) : 0.f;
+// The tensors of an item, by their place in its tile.
+enum : int { kX = 0, kGateA = 1, kGateX = 2, kDy = 3 };
+
+// The rows of one warp's run in global memory, element by element.
+template <typename T, int L>
+struct GlobalRun {
+    static constexpr int kRun = L;
+    static constexpr bool kAdjacent = false;
+    const T *in[4];
+    T *out[3];
+    long long ld[4], ldo[3];
+    int saved;  // the place of its first saved state
+    Lane2<false> l;
+    __device__ GlobalRun(const RecParams &p, int tile, int row0, int saved_) : saved(saved_), l(tile, p.C) {
+        const void *from[4] = {p.x, p.ga, p.gx, p.dy};
+        void *to[3] = {p.y, p.dga, p.dgx};
+        const long long lf[4] = {p.ldx, p.lda, p.ldg, p.lddy}, lt[3] = {p.ldy, p.ld_da, p.ld_dg};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ld[i] = lf[i];
+            in[i] = static_cast<const T *>(from[i]) + static_cast<size_t>(row0) * lf[i];
         }
-    } else {
-        if constexpr (kVec) {
-            r.v = l.ok0 ? __ldcs(reinterpret_cast<const uint32_t *>(row + l.c0)) : 0u;
-        } else {
-            const uint16_t *u = reinterpret_cast<const uint16_t *>(row);
-            r.v = (l.ok0 ? u[l.c0] : 0u) | (l.ok1 ? static_cast<uint32_t>(u[l.c1]) << 16 : 0u);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            ldo[i] = lt[i];
+            out[i] = static_cast<T *>(to[i]) + static_cast<size_t>(row0) * lt[i];
         }
     }
-    return r;
-}
+    __device__ float2 get(int tensor, int j) const { return load2<T>(in[tensor] + j * ld[tensor], l); }
+    __device__ void put(int tensor, int j, float2 f) { store2<T>(out[tensor] + j * ldo[tensor], f, l); }
+    __device__ void done(int) {}
+};
 
-template <typename T, bool kVec>
-__device__ __forceinline__ void store2(T *row, float2 f, const Lane2<T, kVec> &l) {
-    if constexpr (sizeof(T) == 4) {
-        if constexpr (kVec) {
-            if (l.ok0) __stcs(reinterpret_cast<float2 *>(row + l.c0), f);
+// The rows of one warp's run in a tile in shared memory, where the results take the places of the
+// inputs (same tensor, same thread) and leave by one bulk store each -- unless some rows of
+// the run belong to no sequence: those must not be written, so the others go out one by one.
+template <typename T, int kRows, int L>
+struct TileRun {
+    static constexpr int kRun = L;
+    static constexpr bool kAdjacent = true;
+    static constexpr int kRow = kRecTile * sizeof(T), kTensor = kRows * kRow;
+    uint8_t *base;   // this warp's first row
+    const CUtensorMap *maps;  // of the outputs, boxes of L rows
+    const RecParams &p;
+    int tile, row0, saved;
+    bool whole;
+    Lane2<true> l;
+    __device__ TileRun(const RecParams &p_, const CUtensorMap *maps_, uint8_t *stage, int tile_, int row0_, int saved_, int warp, bool whole_)
+        : base(stage + warp * L * kRow), maps(maps_), p(p_), tile(tile_), row0(row0_), saved(saved_), whole(whole_), l(tile_, p_.C) {}
+    __device__ uint8_t *at(int tensor, int j) const {
+        return base + tensor * kTensor + j * kRow + (threadIdx.x & 31) * 2 * static_cast<int>(sizeof(T));
+    }
+    __device__ float2 get(int tensor, int j) const {
+        if constexpr (sizeof(T) == 4) return *reinterpret_cast<const float2 *>(at(tensor, j));
+        const uint32_t v = *reinterpret_cast<const uint32_t *>(at(tensor, j));
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    }
+    __device__ void put(int tensor, int j, float2 f) {
+        if (!whole) {
+            T *out = static_cast<T *>(tensor == 0 ? p.y : tensor == 1 ? p.dga : p.dgx);
+            const long long ld = tensor == 0 ? p.ldy : tensor == 1 ? p.ld_da : p.ld_dg;
+            store2<T>(out + static_cast<size_t>(row0 + j) * ld, f, l);
+        } else if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float2 *>(at(tensor, j)) = f;
         } else {
-            if (l.ok0) row[l.c0] = f.x;
-            if (l.ok1) row[l.c1] = f.y;
-        }
-    } else {
-        if constexpr (kVec) {
-            const __nv_bfloat162 h = __float22bfloat162_rn(f);
-            if (l.ok0) __stcs(reinterpret_cast<uint32_t *>(row + l.c0), *reinterpret_cast<const uint32_t *>(&h));
-        } else {
-            if (l.ok0) row[l.c0] = __float2bfloat16_rn(f.x);
-            if (l.ok1) row[l.c1] = __float2bfloat16_rn(f.y);
+            *reinterpret_cast<__nv_bfloat162 *>(at(tensor, j)) = __float22bfloat162_rn(f);
         }
     }
-}
-
-template <typename T, bool kVec>
-__device__ __forceinline__ float2 load_f32(const float *row, const Lane2<T, kVec> &l) {
-    return row ? make_float2(l.ok0 ? row[l.c0] : 0.f, l.ok1 ? row[l.c1] : 0.f) : make_float2(0.f, 0.f);
-}
-template <typename T, bool kVec>
-__device__ __forceinline__ void store_f32(float *row, float2 f, const Lane2<T, kVec> &l) {
-    if (l.ok0) row[l.c0] = f.x;
-    if (l.ok1) row[l.c1] = f.y;
-}
+    // Sends the results of the first n tensors; the tile is free once lane 0's bulk reads are done.
+    __device__ void done(int n) {
+        if (!whole) return;
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+            for (int i = 0; i < n; ++i) ptx::tma_store_2d(maps + i, base + i * kTensor, tile * kRecTile, row0);
+            ptx::bulk_commit_group();
+        }
+    }
+};
 
 // ----------------------------------------------------------------- the gates ---
 __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
 
 // log2(a) per unit of ra: -kappa softplus(decay) log2(e).
-template <typename T, bool kVec>
-__device__ __forceinline__ float2 decay_rate(const float *decay, float kappa, const Lane2<T, kVec> &l) {
-    const float2 d = load_f32(decay, l);
-    return make_float2(-kappa * kLog2e * softplus(d.x), -kappa * kLog2e * softplus(d.y));
+__device__ __forceinline__ float decay_rate(float decay, float kappa) { return -kappa * kLog2e * softplus(decay); }
+
+template <bool kAdjacent>
+__device__ __forceinline__ float2 decay_rate(const RecParams &p, const Lane2<kAdjacent> &l) {
+    if (p.rates) return load2<float>(p.rates, l);
+    const float2 d = load2<float>(p.decay, l);
+    return make_float2(decay_rate(d.x, p.kappa), decay_rate(d.y, p.kappa));
 }
 
 __device__ __forceinline__ float2 sigmoid2(float2 z) {
@@ -132,28 +201,25 @@ __device__ __forceinline__ float2 sigmoid2(float2 z) {
 // the sigmoids keep that one busy.)
 __device__ __forceinline__ float2 exp2m1(float2 y) {
     y = make_float2(fmaxf(y.x, -126.f), fmaxf(y.y, -126.f));
-    constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number in the low bits
+    constexpr float kRound = 12582912.f + 127.f;  // 1.5 * 2^23 and the exponent's bias: adding it leaves n + 127 in the low bits
     const float2 r = add2(y, splat(kRound));
-    const float2 f = add2(y, mul2(add2(r, splat(-kRound)), splat(-1.f)));
-    const float2 s = make_float2(__int_as_float((__float_as_int(r.x) << 23) + 0x3f800000),
-                                 __int_as_float((__float_as_int(r.y) << 23) + 0x3f800000));
+    const float2 f = fma2(add2(r, splat(-kRound)), splat(-1.f), y);
+    const float2 s = make_float2(__int_as_float(__float_as_int(r.x) << 23), __int_as_float(__float_as_int(r.y) << 23));
     float2 q = fma2(f, splat(0.00015453163f), splat(0.0013390863f));
     q = fma2(f, q, splat(0.009618083f));
     q = fma2(f, q, splat(0.05550357f));
     q = fma2(f, q, splat(0.2402265f));
     q = fma2(f, q, splat(0.6931472f));
     q = mul2(f, q);
-    return fma2(s, q, add2(s, splat(-1.f)));
+    return fma2(s, q, add1(s, -1.f));
 }
 
-// From p = a - 1: beta = sqrt(1 - a^2) and its reciprocal.  1 - a^2 = -p (2 + p) has no
-// cancellation.  Both are 0 where a is 1 to within 1e-37: such a row adds nothing.
-__device__ __forceinline__ void beta_of(float2 p, float2 &beta, float2 &inv) {
-    const float2 v = mul2(mul2(p, splat(-1.f)), add2(p, splat(2.f)));
-    inv = make_float2(v.x > 1e-37f ? rsqrt_approx(v.x) : 0.f, v.y > 1e-37f ? rsqrt_approx(v.y) : 0.f);
-    if (v.x != v.x) inv.x = v.x;
-    if (v.y != v.y) inv.y = v.y;
-    beta = mul2(v, inv);
+// From p = a - 1: minus v, v = 1 - a^2.  -p (2 + p) has no cancellation.
+__device__ __forceinline__ float2 minus_v(float2 p) { return mul2(p, add1(p, 2.f)); }
+// b = beta rx x.  Where a is 1, beta is 0: such a row adds nothing.
+__device__ __forceinline__ float2 contribution(float2 p, float2 rx, float2 x) {
+    const float2 mv = minus_v(p);
+    return mul2(make_float2(sqrt_approx(-mv.x), sqrt_approx(-mv.y)), mul2(rx, x));
 }
 
 // ------------------------------------------------------------------ joining ---
@@ -180,44 +246,61 @@ __device__ __forceinline__ uint64_t peek(const float2 *at) {
     return v;
 }
 
-// Waits, as one warp, for what item `chunk` has published: its carry (returned with A = 0), or
-// its (A, H) unless only the carry will do.  After the time limit it reports and returns zeros.
-template <typename T, bool kVec>
-__device__ __forceinline__ float4 await_item(const RecParams &p, int chunk, bool carry_only, const Lane2<T, kVec> &l) {
-    const size_t at = static_cast<size_t>(chunk) * p.Cpad;
-    uint64_t start = 0;
-    for (unsigned i = 0;; ++i) {
-        const uint32_t c0 = peek(p.carry + at + l.c0), c1 = peek(p.carry + at + l.c1);
-        const uint64_t a0 = peek(p.aggregate + at + l.c0), a1 = peek(p.aggregate + at + l.c1);
-        if (__all_sync(kFull, c0 != kFull && c1 != kFull))
-            return make_float4(0.f, __uint_as_float(c0), 0.f, __uint_as_float(c1));
-        if (!carry_only && __all_sync(kFull, static_cast<uint32_t>(a0) != kFull && static_cast<uint32_t>(a1) != kFull))
-            return make_float4(__uint_as_float(static_cast<uint32_t>(a0)), __uint_as_float(a0 >> 32),
-                               __uint_as_float(static_cast<uint32_t>(a1)), __uint_as_float(a1 >> 32));
-        if ((i & 63u) == 63u) {
-            const uint64_t now = __shfl_sync(kFull, ptx::globaltimer_ns(), 0);
-            if (!start) start = now;
-            else if (now - start > static_cast<uint64_t>(p.timeout_ns)) {
-                if ((threadIdx.x & 31) == 0) atomicExch(p.status, kDevTimeoutCarry);
-                return make_float4(0.f, 0.f, 0.f, 0.f);
+// What the chunks in front of a chunk have published, read by one warp: the nearest kWindow ones.
+constexpr int kWindow = 3;
+template <bool kAdjacent>
+struct Published {
+    uint64_t a0[kWindow], a1[kWindow];
+    uint32_t c0[kWindow], c1[kWindow];
+    // step: +1 where the chunk in front of chunk k is k-1, -1 where it is k+1; `before` of them exist
+    __device__ __forceinline__ void read(const RecParams &p, int chunk, int before, int step, const Lane2<kAdjacent> &l) {
+#pragma unroll
+        for (int i = 0; i < kWindow; ++i) {
+            a0[i] = a1[i] = 0;
+            c0[i] = c1[i] = 0;
+            if (i < before) {
+                const ptrdiff_t at = static_cast<ptrdiff_t>(chunk - step * (i + 1)) * p.Cpad;
+                c0[i] = peek(p.carry + at + l.c0);
+                c1[i] = peek(p.carry + at + l.c1);
+                a0[i] = peek(p.aggregate + at + l.c0);
+                a1[i] = peek(p.aggregate + at + l.c1);
             }
         }
     }
-}
+    // The state that enters the chunk, if it can be told: the nearest carry, and the (A, H) of the
+    // chunks after it, oldest first.
+    __device__ __forceinline__ bool state(float2 &h) const {
+        bool told = true;  // whether all nearer chunks' (A, H) are there
+        int found = -1;
+#pragma unroll
+        for (int i = 0; i < kWindow; ++i) {
+            if (found < 0 && told && __all_sync(kFull, c0[i] != kFull && c1[i] != kFull)) found = i;
+            told = told && __all_sync(kFull, static_cast<uint32_t>(a0[i]) != kFull && static_cast<uint32_t>(a1[i]) != kFull);
+        }
+        if (found < 0) return false;
+#pragma unroll
+        for (int i = kWindow - 1; i >= 0; --i) {
+            if (i == found) h = make_float2(__uint_as_float(c0[i]), __uint_as_float(c1[i]));
+            if (i < found)
+                h = make_float2(after(__uint_as_float(static_cast<uint32_t>(a0[i])), __uint_as_float(a0[i] >> 32), h.x),
+                                after(__uint_as_float(static_cast<uint32_t>(a1[i])), __uint_as_float(a1[i] >> 32), h.y));
+        }
+        return true;
+    }
+};
 
-// What the rows row0 .. row0+L-1 of one warp are, a bit each; `seq` of lane j is row j's sequence.
+// What the rows of a run are, a bit each; `seq` of lane j is row j's sequence.
 struct Run {
     unsigned in, start, end;
     int seq;
 };
-
 template <int L>
-__device__ __forceinline__ Run run_of(const Sequences &q, int row0) {
+__device__ __forceinline__ Run run_of(const Sequences &q, int row0, int limit) {
     const int lane = threadIdx.x & 31, row = row0 + lane;
     Run r;
     r.seq = 0;
     bool in = false, start = false, end = false;
-    if (lane < L && row < q.rows) {
+    if (lane < L && row < limit) {
         const int s = seq_of(q, row);
         if (s >= 0) {
             const int b = seq_begin(q, s), e = seq_begin(q, s + 1);
@@ -233,11 +316,11 @@ __device__ __forceinline__ Run run_of(const Sequences &q, int row0) {
     return r;
 }
 
-// Whether a sequence begins or ends inside the chunk, or rows of it belong to none: then its rows are looked at one by
-// one.  The same for all threads of the block.
-__device__ __forceinline__ bool has_edges(const Sequences &q, int chunk) {
-    const int row0 = chunk * kRecChunk, s = seq_of(q, row0);
-    return s < 0 || seq_begin(q, s) >= row0 || seq_begin(q, s + 1) <= row0 + kRecChunk;
+// Whether a sequence begins or ends inside a chunk, or rows of it belong to none: then its rows are looked at one by
+// one.
+__device__ __forceinline__ bool has_edges(const Sequences &q, int row0, int rows) {
+    const int s = seq_of(q, row0);
+    return s < 0 || seq_begin(q, s) >= row0 || seq_begin(q, s + 1) <= row0 + rows;
 }
 
 __device__ __forceinline__ const float *seq_row(const float *base, const Run &r, int j, int C) {
@@ -245,336 +328,471 @@ __device__ __forceinline__ const float *seq_row(const float *base, const Run &r,
     return base ? base + static_cast<size_t>(s) * C : nullptr;
 }
 
-// Takes the next item; all threads of the block get it.  Without a counter (one chunk: nothing
-// waits for anything) the items are dealt out in turn.
-__device__ __forceinline__ unsigned take_item(const RecParams &p, unsigned *shared) {
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        if (p.ticket) *shared = atomicAdd(p.ticket, 1u) + 1u;
-        else *shared += gridDim.x;
-    }
-    __syncthreads();
-    return *shared;
+// The next item of the block, by one thread.  Without a counter (one chunk: nothing waits for
+// anything) the items are dealt out in turn.
+__device__ __forceinline__ unsigned next_item(const RecParams &p, unsigned &dealt) {
+    if (p.ticket) return atomicAdd(p.ticket, 1u) + 1u;
+    const unsigned item = dealt;
+    dealt += gridDim.x;
+    return item;
 }
 
-// The state that enters a chunk: the nearest published carry of the `n` chunks in front of it
-// (the warps wait for one each), and the (A, H) of those after it, oldest first.  step: +1 where
-// the chunk in front of chunk k is k-1, -1 where it is k+1.
-template <typename T, bool kVec, int W>
-__device__ __forceinline__ float2 carry_in(const RecParams &p, int chunk, int before, int step, float4 (*s_prev)[32],
-                                           int *s_known, const Lane2<T, kVec> &l) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float4 got = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (warp < before) got = await_item(p, chunk - step * (warp + 1), warp == W - 1, l);
-    s_prev[warp][lane] = got;
-    const bool known = __all_sync(kFull, got.x == 0.f && got.z == 0.f);
-    if (lane == 0) s_known[warp] = known;
-    __syncthreads();
-    int j = 0;
-    while (j < W - 1 && !s_known[j]) ++j;
-    float2 h = splat(0.f);
-    for (; j >= 0; --j) {
-        const float4 r = s_prev[j][lane];
-        h = make_float2(after(r.x, r.y, h.x), after(r.z, r.w, h.y));
-    }
-    return h;
+// Shared memory of an item's joining: the runs, and the states that enter them.
+template <int W, bool kBack>
+struct Joins {
+    float4 run[W][32];
+    float2 start[W][32];
+    float2 sum[2][kBack ? W : 1][32];  // backward: the runs' sums of w, of this item and the one before
+    int stop;
+};
+
+// The meetings of the W working warps and the joining warp: the working warps announce their runs, and wait for
+// the states that enter them (false: the block has to stop).
+constexpr int kRunsIn = 1, kStartsIn = 2, kEnd = 3;
+template <int W, bool kBack>
+__device__ __forceinline__ bool exchange(Joins<W, kBack> &s, float4 run, int warp) {
+    s.run[warp][threadIdx.x & 31] = run;
+    __syncwarp();
+    ptx::named_barrier_arrive(kRunsIn, (W + 1) * 32);
+    ptx::named_barrier(kStartsIn, (W + 1) * 32);
+    return *static_cast<volatile int *>(&s.stop) == 0;
 }
 
-// ------------------------------------------------------------------ forward ---
-template <typename T, bool kVec, int W, int L, bool kEdge>
-__device__ __forceinline__ void forward_item(const RecParams &p, int chunk, const Lane2<T, kVec> &l, const Run &run,
-                                             float4 (*s_run)[32], float4 (*s_prev)[32], int *s_known) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row0 = chunk * kRecChunk + warp * L;
-    const T *px = static_cast<const T *>(p.x) + static_cast<size_t>(row0) * p.ldx;
-    const T *pa = static_cast<const T *>(p.ga) + static_cast<size_t>(row0) * p.lda;
-    const T *pg = static_cast<const T *>(p.gx) + static_cast<size_t>(row0) * p.ldg;
-    Raw2<T> rx[L], ra[L], rg[L];
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-        if (!kEdge || (run.in >> j & 1u)) {
-            ra[j] = load2<T, kVec>(pa + j * p.lda, l);
-            rg[j] = load2<T, kVec>(pg + j * p.ldg, l);
-            rx[j] = load2<T, kVec>(px + j * p.ldx, l);
-        }
-    }
-    const float2 rate = decay_rate(p.decay, p.kappa, l);
-    float2 a[L], b[L];
-    float2 A = splat(1.f), H = splat(0.f);
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-        if (kEdge && !(run.in >> j & 1u)) {
-            a[j] = b[j] = A = H = splat(0.f);
-            continue;
-        }
-        const float2 pm = exp2m1(mul2(rate, sigmoid2(ra[j].get())));
-        float2 beta, inv;
-        beta_of(pm, beta, inv);
-        a[j] = add2(pm, splat(1.f));
-        b[j] = mul2(mul2(beta, sigmoid2(rg[j].get())), rx[j].get());
-        if (kEdge && (run.start >> j & 1u)) {
-            const float2 h0 = load_f32(seq_row(p.state, run, j, p.C), l);
-            b[j] = fma2(a[j], h0, b[j]);
-            A = splat(0.f);
-            H = b[j];
-        } else {
-            A = mul2(A, a[j]);
-            H = fma2(a[j], H, b[j]);
-        }
-    }
-    s_run[warp][lane] = make_float4(A.x, H.x, A.y, H.y);
-    if (warp == 0 && lane == 0) s_known[W] = chunk > 0 && (run.in & 1u) && !(run.start & 1u);
-    __syncthreads();
-    const bool needed = s_known[W];  // whether the state of the rows in front enters this chunk
+// Joins a run (A0, H0, A1, H1) to what lies in front of it; without a cut in the chunk a product will do.
+template <bool kEdge>
+__device__ __forceinline__ float4 join(float4 all, float4 r) {
+    if (kEdge) return make_float4(all.x * r.x, after(r.x, r.y, all.y), all.z * r.z, after(r.z, r.w, all.w));
+    const float2 A = make_float2(r.x, r.z), H = fma2(A, make_float2(all.y, all.w), make_float2(r.y, r.w));
+    const float2 P = mul2(make_float2(all.x, all.z), A);
+    return make_float4(P.x, H.x, P.y, H.y);
+}
+template <bool kEdge>
+__device__ __forceinline__ float2 step_over(float4 r, float2 h) {
+    if (kEdge) return make_float2(after(r.x, r.y, h.x), after(r.z, r.w, h.y));
+    return fma2(make_float2(r.x, r.z), h, make_float2(r.y, r.w));
+}
+
+// The joining warp's part of an item: publishes the chunk's (A, H), finds the state that enters the chunk,
+// publishes the one that leaves it, and hands out those that enter the runs.
+template <bool kEdge, bool kForward, int W, bool kAdjacent>
+__device__ __forceinline__ void join_runs(const RecParams &p, int chunk, bool needed, const float4 (*runs)[32],
+                                          float2 (*start)[32], const Lane2<kAdjacent> &l) {
+    constexpr int kStep = kForward ? 1 : -1;
+    const int lane = threadIdx.x & 31;
+    const int before = kForward ? chunk : p.chunks - 1 - chunk;
+    const bool sends = (kForward ? chunk + 1 < p.chunks : chunk > 0) && !p.starve;
     const size_t at = static_cast<size_t>(chunk) * p.Cpad;
+    Published<kAdjacent> front;
+    if (needed) front.read(p, chunk, before, kStep, l);
     float4 all = make_float4(1.f, 0.f, 1.f, 0.f);
-    if (warp == W - 1 && chunk + 1 < p.chunks) {
+    if (sends) {
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const float4 r = s_run[w][lane];
-            all = make_float4(all.x * r.x, after(r.x, r.y, all.y), all.z * r.z, after(r.z, r.w, all.w));
-        }
-        if (needed && !p.starve) {
+        for (int i = 0; i < W; ++i) all = join<kEdge>(all, runs[kForward ? i : W - 1 - i][lane]);
+        if (needed) {
             publish(p.aggregate + at + l.c0, all.x, all.y);
             publish(p.aggregate + at + l.c1, all.z, all.w);
         }
     }
     float2 h = splat(0.f);
-    if (needed) h = carry_in<T, kVec, W>(p, chunk, chunk, 1, s_prev, s_known, l);
-    if (warp == W - 1 && chunk + 1 < p.chunks && !p.starve) {
+    if (needed) {
+        uint64_t began = 0;
+        for (unsigned i = 1; !front.state(h); ++i) {
+            if ((i & 63u) == 0) {
+                const uint64_t now = __shfl_sync(kFull, ptx::globaltimer_ns(), 0);
+                if (!began) began = now;
+                else if (now - began > static_cast<uint64_t>(p.timeout_ns)) {  // report, and go on with zeros
+                    if (lane == 0) atomicExch(p.status, kDevTimeoutCarry);
+                    h = splat(0.f);
+                    break;
+                }
+            }
+            front.read(p, chunk, before, kStep, l);
+        }
+    }
+    if (sends) {
         publish(p.carry + at + l.c0, after(all.x, all.y, h.x));
         publish(p.carry + at + l.c1, after(all.z, all.w, h.y));
     }
-    for (int w = 0; w < warp; ++w) {
-        const float4 r = s_run[w][lane];
-        h = make_float2(after(r.x, r.y, h.x), after(r.z, r.w, h.y));
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const int w = kForward ? i : W - 1 - i;
+        start[w][lane] = h;
+        h = step_over<kEdge>(runs[w][lane], h);
     }
-    T *py = static_cast<T *>(p.y) + static_cast<size_t>(row0) * p.ldy;
+}
+
+// ------------------------------------------------------------------ forward ---
+// A working warp's part of an item.  The run from a zero state: the states H of its rows, and the products A of
+// its decays up to each; with the state h that enters it, A h + H, as the joining has it.
+// `halfway` runs in between, when what was sent before has left.
+template <bool kEdge, int W, typename Rows, typename Halfway>
+__device__ __forceinline__ bool forward_item(const RecParams &p, Rows &rows, const Run &run, Joins<W, false> &s, int warp,
+                                             Halfway halfway) {
+    constexpr int L = Rows::kRun;
+    float2 A[L], H[L];
+    const float2 rate = decay_rate(p, rows.l);
 #pragma unroll
     for (int j = 0; j < L; ++j) {
-        if (kEdge && !(run.in >> j & 1u)) continue;
-        h = kEdge && (run.start >> j & 1u) ? b[j] : fma2(a[j], h, b[j]);
-        store2<T, kVec>(py + j * p.ldy, h, l);
-        if (kEdge && (run.end >> j & 1u) && p.final_state)
-            store_f32(const_cast<float *>(seq_row(p.final_state, run, j, p.C)), h, l);
+        if (j == L / 2) halfway();
+        if (kEdge && !(run.in >> j & 1u)) {
+            A[j] = H[j] = splat(0.f);
+            continue;
+        }
+        const float2 pm = exp2m1(mul2(rate, sigmoid2(rows.get(kGateA, j))));
+        const float2 b = contribution(pm, sigmoid2(rows.get(kGateX, j)), rows.get(kX, j)), a = add1(pm, 1.f);
+        if (kEdge && (run.start >> j & 1u)) {
+            A[j] = splat(0.f);
+            H[j] = fma2(a, load_f32(seq_row(p.state, run, j, p.C), rows.l), b);
+        } else {
+            A[j] = j ? mul2(A[j ? j - 1 : 0], a) : a;
+            H[j] = j ? fma2(a, H[j ? j - 1 : 0], b) : b;
+        }
     }
+    if (!exchange(s, make_float4(A[L - 1].x, H[L - 1].x, A[L - 1].y, H[L - 1].y), warp)) return false;
+    const float2 h = s.start[warp][threadIdx.x & 31];
+    float2 y = h;
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+        if (j % kRecRun == 0 && p.saved) store2(p.saved + static_cast<size_t>(rows.saved + j / kRecRun) * p.Cpad, y, rows.l);
+        if (kEdge && !(run.in >> j & 1u)) continue;
+        y = kEdge ? make_float2(after(A[j].x, H[j].x, h.x), after(A[j].y, H[j].y, h.y)) : fma2(A[j], h, H[j]);
+        rows.put(0, j, y);
+        if (kEdge && (run.end >> j & 1u) && p.final_state)
+            store2(const_cast<float *>(seq_row(p.final_state, run, j, p.C)), y, rows.l);
+    }
+    rows.done(1);
+    return true;
 }
 
 // What a state leaves of an empty sequence: itself.
-template <typename T, bool kVec>
-__device__ __forceinline__ void copy_empty(const Sequences &q, const float *from, float *to, int C, const Lane2<T, kVec> &l) {
+template <int kWarps, bool kAdjacent>
+__device__ __forceinline__ void copy_empty(const Sequences &q, const float *from, float *to, int C, const Lane2<kAdjacent> &l) {
     if (!to) return;
-    for (int s = threadIdx.x >> 5; s < q.nseq; s += blockDim.x >> 5)
+    for (int s = threadIdx.x >> 5; s < q.nseq; s += kWarps)
         if (seq_begin(q, s + 1) <= seq_begin(q, s))
-            store_f32(to + static_cast<size_t>(s) * C, load_f32(from ? from + static_cast<size_t>(s) * C : nullptr, l), l);
-}
-
-template <typename T, bool kVec, int W, int L>
-__global__ void __launch_bounds__(W * 32, 1) rec_forward_kernel(const __grid_constant__ RecParams p) {
-    static_assert(W * L == kRecChunk, "a run of L rows per warp");
-    __shared__ float4 s_run[W][32], s_prev[W][32];
-    __shared__ int s_known[W + 1];
-    __shared__ unsigned s_item;
-    if (threadIdx.x == 0) s_item = blockIdx.x - gridDim.x;
-    const int warp = threadIdx.x >> 5;
-    for (;;) {
-        const unsigned item = take_item(p, &s_item);
-        if (item >= static_cast<unsigned>(p.chunks) * p.tiles) break;
-        const int chunk = item / p.tiles, tile = item - chunk * p.tiles;
-        const Lane2<T, kVec> l(tile, p.C);
-        if (item == 0) check_offsets(p.seq, p.status);
-        if (chunk == 0) copy_empty<T, kVec>(p.seq, p.state, p.final_state, p.C, l);
-        if (has_edges(p.seq, chunk))
-            forward_item<T, kVec, W, L, true>(p, chunk, l, run_of<L>(p.seq, chunk * kRecChunk + warp * L), s_run, s_prev,
-                                              s_known);
-        else
-            forward_item<T, kVec, W, L, false>(p, chunk, l, Run{~0u, 0u, 0u, 0}, s_run, s_prev, s_known);
-    }
+            store2(to + static_cast<size_t>(s) * C, load_f32(from ? from + static_cast<size_t>(s) * C : nullptr, l), l);
 }
 
 // ----------------------------------------------------------------- backward ---
 // With g[t] the gradient of h[t] through everything after it, G[t] = a[t] g[t] is what enters row
 // t-1: G[t] = a[t] (dh[t] + G[t+1]), the same kind of recurrence backwards.  The states are
-// computed again from the forward pass's carries.  Per row, with w = ra d/d(log a):
+// computed again from those that the forward pass kept.  Per row, with w = ra d/d(log a):
 //   dx = g beta rx, d_gate_x = g beta x rx (1-rx), w = a g (h[t-1] - a rx x / beta) ra,
 //   d_gate_a = -kappa softplus(decay) w (1-ra), d_decay = -kappa sigmoid(decay) sum w.
-template <typename T, bool kVec, int W, int L, bool kEdge>
-__device__ __forceinline__ float2 backward_item(const RecParams &p, int chunk, const Lane2<T, kVec> &l, const Run &run,
-                                                float4 (*s_run)[32], float4 (*s_back)[32], float4 (*s_prev)[32],
-                                                int *s_known) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row0 = chunk * kRecChunk + warp * L;
-    const T *px = static_cast<const T *>(p.x) + static_cast<size_t>(row0) * p.ldx;
-    const T *pa = static_cast<const T *>(p.ga) + static_cast<size_t>(row0) * p.lda;
-    const T *pg = static_cast<const T *>(p.gx) + static_cast<size_t>(row0) * p.ldg;
-    const T *pd = static_cast<const T *>(p.dy) + static_cast<size_t>(row0) * p.lddy;
-    const size_t at = static_cast<size_t>(chunk) * p.Cpad;
-    Raw2<T> x[L], dh[L];
-    float2 pm[L], ra[L], rx[L], bh[L];  // a - 1, the gates, and first b, then h[t-1]
-    {
-        Raw2<T> qa[L], qg[L];
-#pragma unroll
-        for (int j = 0; j < L; ++j) {
-            if (!kEdge || (run.in >> j & 1u)) {
-                qa[j] = load2<T, kVec>(pa + j * p.lda, l);
-                qg[j] = load2<T, kVec>(pg + j * p.ldg, l);
-                x[j] = load2<T, kVec>(px + j * p.ldx, l);
-                dh[j] = load2<T, kVec>(pd + j * p.lddy, l);
-            }
-        }
-        const float2 rate = decay_rate(p.decay, p.kappa, l);
-#pragma unroll
-        for (int j = 0; j < L; ++j) {
-            if (kEdge && !(run.in >> j & 1u)) continue;
-            ra[j] = sigmoid2(qa[j].get());
-            rx[j] = sigmoid2(qg[j].get());
-            pm[j] = exp2m1(mul2(rate, ra[j]));
-            float2 beta, inv;
-            beta_of(pm[j], beta, inv);
-            bh[j] = mul2(mul2(beta, rx[j]), x[j].get());
-        }
-    }
-    float2 A = splat(1.f), H = splat(0.f), B = splat(1.f), S = splat(0.f);
+template <bool kEdge, int W, typename Rows, typename Halfway>
+__device__ __forceinline__ bool backward_item(const RecParams &p, Rows &rows, const Run &run, Joins<W, true> &s,
+                                              float2 (*s_sum)[32], int warp, Halfway halfway) {
+    constexpr int L = Rows::kRun;
+    static_assert(L == kRecRun, "a saved state for each run");
+    float2 h = load2<float>(p.saved + static_cast<size_t>(rows.saved) * p.Cpad, rows.l);
+    const float2 rate = decay_rate(p, rows.l);
+    float2 pm[L], ra[L], rx[L], before[L];  // a - 1, the gates, h[t-1]
 #pragma unroll
     for (int j = 0; j < L; ++j) {
-        if (kEdge && !(run.in >> j & 1u)) {
-            A = H = splat(0.f);
-            continue;
-        }
-        const float2 a = add2(pm[j], splat(1.f));
-        if (kEdge && (run.start >> j & 1u)) {
-            H = fma2(a, load_f32(seq_row(p.state, run, j, p.C), l), bh[j]);
-            A = splat(0.f);
-        } else {
-            H = fma2(a, H, bh[j]);
-            A = mul2(A, a);
-        }
+        if (j == L / 2) halfway();
+        if (kEdge && !(run.in >> j & 1u)) continue;
+        ra[j] = sigmoid2(rows.get(kGateA, j));
+        rx[j] = sigmoid2(rows.get(kGateX, j));
+        pm[j] = exp2m1(mul2(rate, ra[j]));
+        if (kEdge && (run.start >> j & 1u)) h = load_f32(seq_row(p.state, run, j, p.C), rows.l);
+        before[j] = h;
+        h = fma2(add1(pm[j], 1.f), h, contribution(pm[j], rx[j], rows.get(kX, j)));
     }
-    if (!kEdge) B = A;
+    // g from zero behind the run, the a of the row after, and the product of all a's so far
+    float2 g = splat(0.f), a = splat(0.f), B = splat(1.f);
 #pragma unroll
     for (int j = L - 1; j >= 0; --j) {
         if (kEdge && !(run.in >> j & 1u)) {
-            B = S = splat(0.f);
+            g = a = B = splat(0.f);
             continue;
         }
-        const float2 a = add2(pm[j], splat(1.f));
+        const float2 dh = rows.get(kDy, j);
         if (kEdge && (run.end >> j & 1u)) {
-            S = mul2(a, add2(dh[j].get(), load_f32(seq_row(p.d_final, run, j, p.C), l)));
+            g = add2(dh, load_f32(seq_row(p.d_final, run, j, p.C), rows.l));
             B = splat(0.f);
         } else {
-            S = mul2(a, add2(dh[j].get(), S));
-            if (kEdge) B = mul2(B, a);
+            g = j < L - 1 ? fma2(a, g, dh) : dh;
         }
+        a = add1(pm[j], 1.f);
+        B = mul2(B, a);
     }
-    s_run[warp][lane] = make_float4(A.x, H.x, A.y, H.y);
-    s_back[warp][lane] = make_float4(B.x, S.x, B.y, S.y);
-    if (lane == 0) {
-        if (warp == 0) s_known[W + 1] = chunk > 0 && (run.in & 1u) && !(run.start & 1u);
-        if (warp == W - 1) s_known[W] = chunk + 1 < p.chunks && (run.in >> (L - 1) & 1u) && !(run.end >> (L - 1) & 1u);
-    }
-    __syncthreads();
-    const bool needed = s_known[W];  // whether the rows behind this chunk send a gradient into it
-    float4 all = make_float4(1.f, 0.f, 1.f, 0.f);
-    if (warp == 0 && chunk > 0) {
-#pragma unroll
-        for (int w = W - 1; w >= 0; --w) {
-            const float4 r = s_back[w][lane];
-            all = make_float4(all.x * r.x, after(r.x, r.y, all.y), all.z * r.z, after(r.z, r.w, all.w));
-        }
-        if (needed && !p.starve) {
-            publish(p.aggregate + at + l.c0, all.x, all.y);
-            publish(p.aggregate + at + l.c1, all.z, all.w);
-        }
-    }
-    // the states again
-    float2 h = splat(0.f);
-    if (s_known[W + 1]) {
-        const float *saved = p.saved + at - p.Cpad;
-        h = make_float2(saved[l.c0], saved[l.c1]);
-    }
-    for (int w = 0; w < warp; ++w) {
-        const float4 r = s_run[w][lane];
-        h = make_float2(after(r.x, r.y, h.x), after(r.z, r.w, h.y));
-    }
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-        if (kEdge && !(run.in >> j & 1u)) continue;
-        if (kEdge && (run.start >> j & 1u)) h = load_f32(seq_row(p.state, run, j, p.C), l);
-        const float2 b = bh[j];
-        bh[j] = h;
-        h = fma2(add2(pm[j], splat(1.f)), h, b);
-    }
-    float2 G = splat(0.f);
-    if (needed) G = carry_in<T, kVec, W>(p, chunk, p.chunks - 1 - chunk, -1, s_prev, s_known, l);
-    if (warp == 0 && chunk > 0 && !p.starve) {
-        publish(p.carry + at + l.c0, after(all.x, all.y, G.x));
-        publish(p.carry + at + l.c1, after(all.z, all.w, G.y));
-    }
-    for (int w = W - 1; w > warp; --w) {
-        const float4 r = s_back[w][lane];
-        G = make_float2(after(r.x, r.y, G.x), after(r.z, r.w, G.y));
-    }
-    const float2 rate = mul2(decay_rate(p.decay, p.kappa, l), splat(1.f / kLog2e));
-    T *ox = static_cast<T *>(p.y) + static_cast<size_t>(row0) * p.ldy;
-    T *oa = static_cast<T *>(p.dga) + static_cast<size_t>(row0) * p.ld_da;
-    T *og = static_cast<T *>(p.dgx) + static_cast<size_t>(row0) * p.ld_dg;
+    const float2 S = mul2(a, g);
+    if (!exchange(s, make_float4(B.x, S.x, B.y, S.y), warp)) return false;
+    const float2 G = s.start[warp][threadIdx.x & 31];
+    const float2 natural = mul2(decay_rate(p, rows.l), splat(1.f / kLog2e));
     float2 sum = splat(0.f);
+    g = a = splat(0.f);
 #pragma unroll
     for (int j = L - 1; j >= 0; --j) {
-        if (kEdge && !(run.in >> j & 1u)) continue;
-        if (kEdge && (run.end >> j & 1u)) G = load_f32(seq_row(p.d_final, run, j, p.C), l);
-        const float2 a = add2(pm[j], splat(1.f));
-        const float2 g = add2(dh[j].get(), G);
-        G = mul2(a, g);
-        float2 beta, inv;
-        beta_of(pm[j], beta, inv);
-        const float2 xv = x[j].get();
-        const float2 dx = mul2(g, mul2(beta, rx[j]));
-        const float2 minus_ra = mul2(ra[j], splat(-1.f)), minus_rx = mul2(rx[j], splat(-1.f));
-        const float2 dg = mul2(mul2(dx, xv), add2(minus_rx, splat(1.f)));
-        const float2 w = mul2(mul2(G, ra[j]), fma2(mul2(a, inv), mul2(minus_rx, xv), bh[j]));
-        sum = add2(sum, w);
-        const float2 da = mul2(mul2(rate, w), add2(minus_ra, splat(1.f)));
-        store2<T, kVec>(ox + j * p.ldy, dx, l);
-        store2<T, kVec>(oa + j * p.ld_da, da, l);
-        store2<T, kVec>(og + j * p.ld_dg, dg, l);
+        if (kEdge && !(run.in >> j & 1u)) {
+            g = a = splat(0.f);
+            continue;
+        }
+        const float2 dh = rows.get(kDy, j), x = rows.get(kX, j);
+        if (kEdge && (run.end >> j & 1u)) g = add2(dh, load_f32(seq_row(p.d_final, run, j, p.C), rows.l));
+        else g = j < L - 1 ? fma2(a, g, dh) : add2(dh, G);
+        a = add1(pm[j], 1.f);
+        const float2 back = mul2(a, g), ga = mul2(ra[j], back), bx = mul2(rx[j], x);
+        // 1 / beta; 1e-37 under the root keeps it finite where a is 1 and ra, beta and so all but dh's share are 0
+        const float2 mv = minus_v(pm[j]);
+        const float2 under = fma2(mv, splat(-1.f), splat(1e-37f));
+        const float2 inv = make_float2(rsqrt_approx(under.x), rsqrt_approx(under.y));
+        const float2 dx = mul2(mul2(g, rx[j]), negative(mul2(mv, inv)));
+        const float2 dg = mul2(mul2(dx, x), one_minus(rx[j]));
+        const float2 inner = fma2(negative(mul2(a, inv)), bx, before[j]);
+        const float2 w = mul2(ga, inner);
+        sum = fma2(ga, inner, sum);
+        const float2 da = mul2(mul2(natural, w), one_minus(ra[j]));
+        rows.put(0, j, dx);
+        rows.put(1, j, da);
+        rows.put(2, j, dg);
         if (kEdge && (run.start >> j & 1u) && p.d_state)
-            store_f32(const_cast<float *>(seq_row(p.d_state, run, j, p.C)), G, l);
+            store2(const_cast<float *>(seq_row(p.d_state, run, j, p.C)), back, rows.l);
     }
-    return sum;
+    rows.done(3);
+    s_sum[warp][threadIdx.x & 31] = sum;
+    return true;
 }
 
-template <typename T, bool kVec, int W, int L>
-__global__ void __launch_bounds__(W * 32, 1) rec_backward_kernel(const __grid_constant__ RecParams p) {
-    static_assert(W * L == kRecChunk, "a run of L rows per warp");
-    __shared__ float4 s_run[W][32], s_back[W][32], s_prev[W][32];
-    __shared__ float2 s_sum[W][32];
-    __shared__ int s_known[W + 2];
-    __shared__ unsigned s_item;
-    if (threadIdx.x == 0) s_item = blockIdx.x - gridDim.x;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (;;) {
-        const unsigned item = take_item(p, &s_item);
-        if (item >= static_cast<unsigned>(p.chunks) * p.tiles) break;
-        const int chunk = p.chunks - 1 - static_cast<int>(item / p.tiles), tile = item % p.tiles;
-        const Lane2<T, kVec> l(tile, p.C);
-        if (item == 0) check_offsets(p.seq, p.status);
-        if (chunk == 0) copy_empty<T, kVec>(p.seq, p.d_final, p.d_state, p.C, l);
-        if (has_edges(p.seq, chunk))
-            s_sum[warp][lane] = backward_item<T, kVec, W, L, true>(
-                p, chunk, l, run_of<L>(p.seq, chunk * kRecChunk + warp * L), s_run, s_back, s_prev, s_known);
-        else
-            s_sum[warp][lane] = backward_item<T, kVec, W, L, false>(p, chunk, l, Run{~0u, 0u, 0u, 0}, s_run, s_back,
-                                                                    s_prev, s_known);
-        __syncthreads();
-        if (warp == 0) {  // the chunk's sum of w, its warps' in order
-            float2 sum = splat(0.f);
+template <bool kEdge, int W, bool kBack, typename Rows, typename Halfway>
+__device__ __forceinline__ bool work_item(const RecParams &p, Rows &rows, const Run &run, Joins<W, kBack> &s, float2 (*s_sum)[32],
+                                          int warp, Halfway halfway) {
+    if constexpr (kBack) return backward_item<kEdge, W>(p, rows, run, s, s_sum, warp, halfway);
+    else return forward_item<kEdge, W>(p, rows, run, s, warp, halfway);
+}
+// The form for chunks with edges, as a call: inlined, it would take registers from the other.
+template <int W, bool kBack, typename Rows, typename Halfway>
+__device__ __noinline__ bool work_item_edges(const RecParams &p, Rows rows, Run run, Joins<W, kBack> &s, float2 (*s_sum)[32],
+                                             int warp, Halfway halfway) {
+    return work_item<true, W, kBack>(p, rows, run, s, s_sum, warp, halfway);
+}
+
+// The chunk's sum of w, its warps' in order.
+template <int W, bool kAdjacent>
+__device__ __forceinline__ void store_sum(const RecParams &p, int chunk, const float2 (*s_sum)[32], const Lane2<kAdjacent> &l) {
+    float2 sum = splat(0.f);
 #pragma unroll
-            for (int w = 0; w < W; ++w) sum = add2(sum, s_sum[w][lane]);
-            float *out = p.decay_partial + static_cast<size_t>(chunk) * p.Cpad;
-            out[l.c0] = sum.x;
-            out[l.c1] = sum.y;
+    for (int w = 0; w < W; ++w) sum = add2(sum, s_sum[w][threadIdx.x & 31]);
+    float *out = p.decay_partial + static_cast<size_t>(chunk) * p.Cpad;
+    out[l.c0] = sum.x;
+    out[l.c1] = sum.y;
+}
+
+// ------------------------------------------------------------------ kernels ---
+// Where the chunks lie.  Either they follow one another over all rows, or each sequence has its own
+// (p.per_seq of them): then the items go round the sequences, and a chunk follows the one in front of it so
+// many items later that it hardly ever waits.
+__device__ __forceinline__ int chunk_row(const RecParams &p, int chunk, int chunk_rows) {
+    if (!p.per_seq) return chunk * chunk_rows;
+    const int s = chunk / p.per_seq;
+    return s * p.seq.T + (chunk - s * p.per_seq) * chunk_rows;
+}
+// The end of the rows that a chunk may have.
+__device__ __forceinline__ int chunk_limit(const RecParams &p, int chunk) {
+    return p.per_seq ? (chunk / p.per_seq + 1) * p.seq.T : p.seq.rows;
+}
+
+// The place of the first saved state of a run: one for every kRecRun rows, counted in each sequence if it has chunks of its own.
+__device__ __forceinline__ int saved_place(const RecParams &p, int chunk, int row0) {
+    if (!p.per_seq) return row0 / kRecRun;
+    const int s = chunk / p.per_seq;
+    return s * ((p.seq.T + kRecRun - 1) / kRecRun + kRecSavedSpare) + (row0 - s * p.seq.T) / kRecRun;
+}
+
+// An item.
+struct Item {
+    int chunk;  // -1: no more items
+    int tile, row0;
+    int saved;  // saved_place of its first run
+    int flags;  // kEdges: has edges; kFirst: the first of all
+};
+enum : int { kEdges = 1, kFirst = 2 };
+
+__device__ __forceinline__ Item item_of(const RecParams &p, unsigned item, int chunk_rows, bool back) {
+    if (item >= static_cast<unsigned>(p.chunks) * p.tiles) return Item{-1, 0, 0, 0, 0};
+    const int turn = item / p.tiles, tile = item - turn * p.tiles;
+    int chunk = back ? p.chunks - 1 - turn : turn;
+    if (p.per_seq) {
+        const int k = turn / p.seq.nseq, s = turn - k * p.seq.nseq;
+        chunk = s * p.per_seq + (back ? p.per_seq - 1 - k : k);
+    }
+    const int row0 = chunk_row(p, chunk, chunk_rows);
+    return Item{chunk, tile, row0, saved_place(p, chunk, row0), (has_edges(p.seq, row0, chunk_rows) ? kEdges : 0) | (item == 0 ? kFirst : 0)};
+}
+
+// The joining warp's work on an item.
+template <int W, int L, bool kBack, bool kAdjacent>
+__device__ __forceinline__ void join_item(const RecParams &p, const Item &item, const float4 (*runs)[32], float2 (*start)[32],
+                                          const Lane2<kAdjacent> &l) {
+    const int chunk = item.chunk;
+    // whether the rows in front of the chunk (against the order of time: behind it) reach into it
+    bool needed = kBack ? chunk + 1 < p.chunks : chunk > 0;
+    if (!(item.flags & kEdges)) {
+        join_runs<false, !kBack, W>(p, chunk, needed, runs, start, l);
+        return;
+    }
+    if (p.per_seq) {
+        needed = (kBack ? chunk + 1 : chunk) % p.per_seq != 0;
+    } else if (needed) {
+        const int row0 = item.row0, row1 = row0 + W * L, s = seq_of(p.seq, kBack ? row1 - 1 : row0);
+        needed = s >= 0 && (kBack ? row1 < seq_begin(p.seq, s + 1) : seq_begin(p.seq, s) < row0 && row0 < seq_begin(p.seq, s + 1));
+    }
+    join_runs<true, !kBack, W>(p, chunk, needed, runs, start, l);
+}
+
+// Items element by element, for tensors that TMA does not take.
+template <typename T, int W, int L, bool kBack>
+__global__ void __launch_bounds__((W + 1) * 32, 2) rec_plain_kernel(const __grid_constant__ RecParams p) {
+    __shared__ Joins<W, kBack> s;
+    __shared__ Item s_item;
+    const int warp = threadIdx.x >> 5;
+    unsigned dealt = blockIdx.x;
+    if (threadIdx.x == 0) s.stop = 0;
+    for (;;) {
+        __syncthreads();
+        if (threadIdx.x == 0) s_item = item_of(p, next_item(p, dealt), W * L, kBack);
+        __syncthreads();
+        const Item item = s_item;
+        if (item.chunk < 0) break;
+        const int row0 = item.row0 + warp * L;
+        GlobalRun<T, L> rows(p, item.tile, row0, item.saved + warp * L / kRecRun);
+        if (item.flags & kFirst) check_offsets(p.seq, p.status);
+        if (item.chunk == 0)
+            copy_empty<W + 1>(p.seq, kBack ? p.d_final : p.state, kBack ? p.d_state : p.final_state, p.C, rows.l);
+        auto nothing = [] {};
+        if (warp == W) {
+            ptx::named_barrier(kRunsIn, (W + 1) * 32);
+            join_item<W, L, kBack>(p, item, s.run, s.start, rows.l);
+            ptx::named_barrier_arrive(kStartsIn, (W + 1) * 32);
+        } else if (item.flags & kEdges) {
+            work_item_edges<W, kBack>(p, rows, run_of<L>(p.seq, row0, chunk_limit(p, item.chunk)), s, s.sum[0], warp, nothing);
+        } else {
+            work_item<false, W, kBack>(p, rows, Run{~0u, 0u, 0u, 0}, s, s.sum[0], warp, nothing);
         }
+        if constexpr (kBack) {
+            __syncthreads();
+            if (warp == W) store_sum<W>(p, item.chunk, s.sum[0], rows.l);
+        }
+    }
+}
+
+// Items in tiles that travel by TMA through S stages of shared memory.  The joining warp also takes the items and
+// issues their loads.
+template <typename T, int W, int L, int S, bool kBack, int kBlocks>
+__global__ void __launch_bounds__((W + 1) * 32, kBlocks) rec_tile_kernel(const __grid_constant__ RecTiles q) {
+    static_assert(S >= 2, "one item at work, one on its way");
+    using Tile = TileRun<T, W * L, L>;
+    constexpr int kIn = kBack ? 4 : 3, kAll = (W + 1) * 32;
+    constexpr int kStage = kIn * Tile::kTensor;
+    extern __shared__ __align__(128) uint8_t s_tiles[];
+    __shared__ Joins<W, kBack> s;
+    __shared__ uint64_t s_full[S], s_free;  // a stage's loads have come; the last item's results have left
+    __shared__ Item s_item[S];
+    __shared__ int s_abort;
+    const RecParams &p = q.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        s_abort = s.stop = 0;
+        for (int i = 0; i < S; ++i) ptx::mbar_init(&s_full[i], 1);
+        ptx::mbar_init(&s_free, W);
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    const ptx::Watchdog wd{&s_abort, p.status, static_cast<uint64_t>(p.timeout_ns)};
+    if (warp == W) {
+        unsigned dealt = blockIdx.x;
+        Item ahead{-1, 0, 0, 0, 0};  // lane 0: the item to be loaded next, taken while nothing waits for it
+        auto take = [&] {
+            if (lane == 0) ahead = item_of(p, next_item(p, dealt), W * L, kBack);
+        };
+        auto issue = [&](int stage) {  // its loads
+            if (lane == 0) {
+                s_item[stage] = ahead;
+                if (ahead.chunk < 0) {
+                    ptx::mbar_arrive(&s_full[stage]);
+                } else {
+                    ptx::fence_proxy_async_smem();
+                    ptx::mbar_arrive_expect_tx(&s_full[stage], kStage);
+#pragma unroll
+                    for (int i = 0; i < kIn; ++i)
+                        ptx::tma_load_2d(s_tiles + stage * kStage + i * Tile::kTensor, &q.in[i], &s_full[stage],
+                                         ahead.tile * kRecTile, ahead.row0);
+                }
+            }
+            __syncwarp();
+        };
+        for (int i = 0; i < S; ++i) {
+            take();
+            issue(i);
+        }
+        take();
+        int2 one = make_int2(-1, 0);  // chunk and tile of the item before
+        unsigned n = 0;
+        bool stop = false;
+        for (;; ++n) {
+            const Item item = s_item[n % S];
+            if (item.chunk < 0) break;
+            const Lane2<true> l(item.tile, p.C);
+            if (item.flags & kFirst) check_offsets(p.seq, p.status, lane, 32);
+            ptx::mbar_wait(&s_free, n & 1u, wd, kDevTimeoutEmpty);
+            if (n > 0) issue((n - 1) % S);
+            ptx::named_barrier(kRunsIn, kAll);
+            stop = *static_cast<volatile int *>(&s_abort) != 0;
+            if (stop) s.stop = 1;
+            else join_item<W, L, kBack>(p, item, s.run, s.start, l);
+            __syncwarp();
+            ptx::named_barrier_arrive(kStartsIn, kAll);
+            if (stop) break;
+            if constexpr (kBack) {
+                if (one.x >= 0) store_sum<W>(p, one.x, s.sum[~n & 1], Lane2<true>(one.y, p.C));
+            }
+            if (n > 0) take();
+            one = make_int2(item.chunk, item.tile);
+        }
+        if (stop) {
+            if (lane == 0) {  // a load did not come: wait, within the limit, for those in flight
+                s_abort = 0;
+                const unsigned issued = n ? n + S : S;  // turns whose loads were issued
+                for (unsigned i = n; i < issued; ++i) ptx::mbar_wait(&s_full[i % S], i / S & 1u, wd, kDevTimeoutFull);
+            }
+        } else if constexpr (kBack) {
+            ptx::named_barrier(kEnd, kAll);
+            if (one.x >= 0) store_sum<W>(p, one.x, s.sum[~n & 1], Lane2<true>(one.y, p.C));
+        }
+        return;
+    }
+    // the results of the item before have left its stage
+    auto halfway = [&] {
+        if (lane == 0) {
+            ptx::bulk_wait_group_read<0>();
+            ptx::mbar_arrive(&s_free);
+        }
+    };
+    int stage = 0;
+    unsigned parity = 0;
+    bool fine = true;
+    for (unsigned n = 0;; ++n) {
+        ptx::mbar_wait(&s_full[stage], parity, wd, kDevTimeoutFull);  // a failure stops the block at the joining
+        const Item item = s_item[stage];
+        if (item.chunk < 0) break;
+        const bool edges = item.flags & kEdges;
+        const int row0 = item.row0 + warp * L;
+        const Run run = edges ? run_of<L>(p.seq, row0, chunk_limit(p, item.chunk)) : Run{~0u, 0u, 0u, 0};
+        Tile rows(p, q.out, s_tiles + stage * kStage, item.tile, row0, item.saved + warp * L / kRecRun, warp,
+                  (run.in & ((1u << L) - 1u)) == (1u << L) - 1u);
+        if (item.chunk == 0)
+            copy_empty<W>(p.seq, kBack ? p.d_final : p.state, kBack ? p.d_state : p.final_state, p.C, rows.l);
+        fine = edges ? work_item_edges<W, kBack>(p, rows, run, s, s.sum[n & 1], warp, halfway)
+                     : work_item<false, W, kBack>(p, rows, run, s, s.sum[n & 1], warp, halfway);
+        if (!fine) break;
+        if (++stage == S) {
+            stage = 0;
+            parity ^= 1u;
+        }
+    }
+    if (lane == 0) ptx::bulk_wait_group_read<0>();
+    if constexpr (kBack) {
+        if (fine) ptx::named_barrier(kEnd, kAll);
     }
 }
 
@@ -600,70 +818,107 @@ __global__ void __launch_bounds__(1024) rec_decay_kernel(const float *partial, c
     }
 }
 
-// All ones in the counter and the arrays whose values are their own flags.
-__global__ void __launch_bounds__(256) rec_init_kernel(uint32_t *a, size_t na, uint32_t *b, size_t nb) {
-    const size_t step = static_cast<size_t>(gridDim.x) * blockDim.x;
-    for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < na + nb; i += step)
-        (i < na ? a : b - na)[i] = kFull;
+// All ones in the counter and the arrays whose values are their own flags; the decay rates of the channels.
+__global__ void __launch_bounds__(256) rec_init_kernel(uint4 *words, size_t n, const float *decay, float kappa, float *rates,
+                                                       int C) {
+    const size_t step = static_cast<size_t>(gridDim.x) * blockDim.x, i0 = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x;
+    for (size_t i = i0; i < n; i += step) words[i] = make_uint4(kFull, kFull, kFull, kFull);
+    for (size_t c = i0; c < static_cast<size_t>(C); c += step) rates[c] = decay_rate(decay[c], kappa);
 }
 
 // One token: a block takes 256 channels of one row.
-template <typename T, bool kVec>
+template <typename T>
 __global__ void __launch_bounds__(128) rec_step_kernel(const __grid_constant__ RecStepParams p) {
     const int b = blockIdx.x / p.tiles;
-    const Lane2<T, kVec> l(blockIdx.x % p.tiles * 4 + (threadIdx.x >> 5), p.C);
+    const Lane2<false> l(blockIdx.x % p.tiles * 4 + (threadIdx.x >> 5), p.C);
     const int slot = p.slots ? p.slots[b] : b;
-    const float2 x = load2<T, kVec>(static_cast<const T *>(p.x) + static_cast<size_t>(b) * p.ldx, l).get();
-    const float2 ga = load2<T, kVec>(static_cast<const T *>(p.ga) + static_cast<size_t>(b) * p.lda, l).get();
-    const float2 gx = load2<T, kVec>(static_cast<const T *>(p.gx) + static_cast<size_t>(b) * p.ldg, l).get();
-    const float2 rate = decay_rate(p.decay, p.kappa, l);
+    const float2 x = load2<T>(static_cast<const T *>(p.x) + static_cast<size_t>(b) * p.ldx, l);
+    const float2 ga = load2<T>(static_cast<const T *>(p.ga) + static_cast<size_t>(b) * p.lda, l);
+    const float2 gx = load2<T>(static_cast<const T *>(p.gx) + static_cast<size_t>(b) * p.ldg, l);
+    const float2 decay = load2<float>(p.decay, l);
     if (slot < 0 || slot >= p.pool) return;
     float *state = p.state + static_cast<size_t>(slot) * p.C;
-    const float2 h0 = load_f32(state, l);
+    const float2 h0 = load2<float>(state, l);
     if (p.slots && slot_named_before(p.slots, b, slot)) {
         if (threadIdx.x == 0) atomicExch(p.status, kDevBadSlot);
         return;
     }
+    const float2 rate = make_float2(decay_rate(decay.x, p.kappa), decay_rate(decay.y, p.kappa));
     const float2 pm = exp2m1(mul2(rate, sigmoid2(ga)));
-    float2 beta, inv;
-    beta_of(pm, beta, inv);
-    const float2 h = fma2(add2(pm, splat(1.f)), h0, mul2(mul2(beta, sigmoid2(gx)), x));
-    store2<T, kVec>(static_cast<T *>(p.y) + static_cast<size_t>(b) * p.ldy, h, l);
-    store_f32(state, h, l);
+    const float2 h = fma2(add1(pm, 1.f), h0, contribution(pm, sigmoid2(gx), x));
+    store2<T>(static_cast<T *>(p.y) + static_cast<size_t>(b) * p.ldy, h, l);
+    store2<float>(state, h, l);
 }
 
+// Resident blocks of a kernel, looked up once per device (and its shared memory allowed).
 template <typename K>
-cudaError_t launch_items(K kernel, const RecParams &p, int threads, int sms, cudaStream_t s) {
-    int per_sm = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+cudaError_t resident_blocks(K kernel, int threads, size_t smem, std::atomic<int> *known, int *blocks) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    *blocks = dev < kMaxKnown ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (*blocks) return cudaSuccess;
+    if (smem) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
+    int per_sm = 0, sms = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    *blocks = (per_sm < 1 ? 1 : per_sm) * sms;
+    if (dev < kMaxKnown) known[dev].store(*blocks, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+int grid_of(const RecParams &p, int blocks) {
     const long long items = static_cast<long long>(p.chunks) * p.tiles;
-    const long long room = static_cast<long long>(per_sm < 1 ? 1 : per_sm) * sms;
-    kernel<<<static_cast<int>(items < room ? items : room), threads, 0, s>>>(p);
+    return static_cast<int>(items < blocks ? items : blocks);
+}
+
+template <typename T, bool kBack>
+cudaError_t launch_plain(const RecParams &p, cudaStream_t s) {
+    constexpr RecShape k = rec_shape(sizeof(T), kBack);
+    static std::atomic<int> known[kMaxKnown];
+    int blocks = 0;
+    const auto kernel = rec_plain_kernel<T, k.warps, k.run, kBack>;
+    const cudaError_t e = resident_blocks(kernel, (k.warps + 1) * 32, 0, known, &blocks);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid_of(p, blocks), (k.warps + 1) * 32, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, bool kBack>
+cudaError_t launch_tiles(const RecTiles &q, cudaStream_t s) {
+    constexpr RecShape k = rec_shape(sizeof(T), kBack);
+    constexpr size_t smem = static_cast<size_t>(k.stages) * (kBack ? 4 : 3) * TileRun<T, k.warps * k.run, k.run>::kTensor;
+    static std::atomic<int> known[kMaxKnown];
+    int blocks = 0;
+    const auto kernel = rec_tile_kernel<T, k.warps, k.run, k.stages, kBack, k.blocks>;
+    const cudaError_t e = resident_blocks(kernel, (k.warps + 1) * 32, smem, known, &blocks);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid_of(q.p, blocks), (k.warps + 1) * 32, smem, s>>>(q);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_rec_init(const RecParams &p, size_t words, float *carry, size_t carry_words, cudaStream_t s) {
-    const size_t blocks = (words + carry_words + 1023) / 1024;
-    rec_init_kernel<<<static_cast<int>(blocks < 592 ? blocks : 592), 256, 0, s>>>(
-        p.ticket, words, reinterpret_cast<uint32_t *>(carry), carry_words);
+// `words`: a multiple of 4.
+cudaError_t launch_rec_init(const RecParams &p, size_t words, float *rates, cudaStream_t s) {
+    const size_t blocks = (words / 4 + 255) / 256;
+    rec_init_kernel<<<static_cast<int>(blocks < 592 ? blocks : 592), 256, 0, s>>>(reinterpret_cast<uint4 *>(p.ticket), words / 4,
+                                                                                  p.decay, p.kappa, rates, p.C);
     return cudaGetLastError();
 }
 
-cudaError_t launch_rec_forward(const RecParams &p, bool f32, bool vec, int sms, cudaStream_t s) {
-    if (f32) return vec ? launch_items(rec_forward_kernel<float, true, 16, 8>, p, 512, sms, s)
-                        : launch_items(rec_forward_kernel<float, false, 16, 8>, p, 512, sms, s);
-    return vec ? launch_items(rec_forward_kernel<__nv_bfloat16, true, 16, 8>, p, 512, sms, s)
-               : launch_items(rec_forward_kernel<__nv_bfloat16, false, 16, 8>, p, 512, sms, s);
+cudaError_t launch_rec_plain(const RecParams &p, bool f32, bool back, cudaStream_t s) {
+    if (f32) return back ? launch_plain<float, true>(p, s) : launch_plain<float, false>(p, s);
+    return back ? launch_plain<__nv_bfloat16, true>(p, s) : launch_plain<__nv_bfloat16, false>(p, s);
 }
 
-cudaError_t launch_rec_backward(const RecParams &p, bool f32, bool vec, int sms, cudaStream_t s) {
-    if (f32) return vec ? launch_items(rec_backward_kernel<float, true, 16, 8>, p, 512, sms, s)
-                        : launch_items(rec_backward_kernel<float, false, 16, 8>, p, 512, sms, s);
-    return vec ? launch_items(rec_backward_kernel<__nv_bfloat16, true, 16, 8>, p, 512, sms, s)
-               : launch_items(rec_backward_kernel<__nv_bfloat16, false, 16, 8>, p, 512, sms, s);
+cudaError_t launch_rec_tiles(const RecTiles &q, bool f32, bool back, cudaStream_t s) {
+    if (f32) return back ? launch_tiles<float, true>(q, s) : launch_tiles<float, false>(q, s);
+    return back ? launch_tiles<__nv_bfloat16, true>(q, s) : launch_tiles<__nv_bfloat16, false>(q, s);
 }
 
 cudaError_t launch_rec_decay(const float *partial, const float *decay, float kappa, float *d_decay, int chunks, int C,
@@ -672,14 +927,9 @@ cudaError_t launch_rec_decay(const float *partial, const float *decay, float kap
     return cudaGetLastError();
 }
 
-cudaError_t launch_rec_step(const RecStepParams &p, bool f32, bool vec, cudaStream_t s) {
-    if (f32) {
-        if (vec) rec_step_kernel<float, true><<<p.B * p.tiles, 128, 0, s>>>(p);
-        else rec_step_kernel<float, false><<<p.B * p.tiles, 128, 0, s>>>(p);
-    } else {
-        if (vec) rec_step_kernel<__nv_bfloat16, true><<<p.B * p.tiles, 128, 0, s>>>(p);
-        else rec_step_kernel<__nv_bfloat16, false><<<p.B * p.tiles, 128, 0, s>>>(p);
-    }
+cudaError_t launch_rec_step(const RecStepParams &p, bool f32, cudaStream_t s) {
+    if (f32) rec_step_kernel<float><<<p.B * p.tiles, 128, 0, s>>>(p);
+    else rec_step_kernel<__nv_bfloat16><<<p.B * p.tiles, 128, 0, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -58,16 +58,26 @@ struct RecParams {
     const float *d_final;  // backward: gradient of final_state, or NULL
     float *d_state;        // backward: gradient of state, or NULL
     float *decay_partial;  // backward: [chunks][Cpad] sums
-    const float *saved;    // backward: the forward pass's carries
-    float *carry;          // [chunks][Cpad] carries behind each chunk (forward: the saved states)
+    float *saved;          // [runs][Cpad] the state that enters each run of kRecRun rows: written by the forward pass (or
+                           // NULL), read by the backward pass
+    const float *rates;    // (C,) decay rates from the start of the call, or NULL (computed on the spot)
+    float *carry;          // [chunks][Cpad] carries behind each chunk (against the order of time: in front)
     float2 *aggregate;     // [chunks][Cpad] (product of decays, state of a zero start)
     unsigned *ticket;      // starts at 0xffffffff
     long long ldx, lda, ldg, ldy, lddy, ld_da, ld_dg;
     Sequences seq;
     int C, Cpad, tiles, chunks;
+    int per_seq;           // chunks of each sequence; 0: the chunks follow one another over all rows
     int *status;
     long long timeout_ns;
     int starve;
+};
+
+// The recurrence in tiles that travel by TMA.
+struct RecTiles {
+    CUtensorMap in[4];     // x, gate_a, gate_x, dy as {C, rows}: boxes of kRecTile x a chunk's rows
+    CUtensorMap out[3];    // y, or dx, d_gate_a, d_gate_x: boxes of kRecTile x a run's rows
+    RecParams p;
 };
 
 struct RecStepParams {
@@ -83,8 +93,18 @@ struct RecStepParams {
 };
 
 constexpr int kConvWarps = 4;     // warps of a conv1d block, one strip of rows each
-constexpr int kRecChunk = 128;    // rows of one work item of the recurrence, and of one saved carry
-constexpr int kRecTile = 64;      // channels of one work item
+constexpr int kRecTile = 64;      // channels of a work item of the recurrence
+constexpr int kRecRun = 8;        // rows of one saved state
+constexpr int kRecSavedSpare = 32;  // saved states of rows behind a sequence's last one, in its last chunk
+
+// How a kernel of the recurrence is laid out: working warps, rows that one scans, stages of shared memory, blocks an SM.
+struct RecShape {
+    int warps, run, stages, blocks;
+    constexpr int rows() const { return warps * run; }
+};
+constexpr RecShape rec_shape(int elt, bool back) {
+    return back ? (elt == 2 ? RecShape{7, 8, 2, 2} : RecShape{6, 8, 2, 2}) : (elt == 2 ? RecShape{8, 16, 2, 2} : RecShape{8, 8, 2, 2});
+}
 
 cudaError_t launch_conv1d_forward(const Conv1dParams &p, bool f32, bool vec, cudaStream_t s);
 cudaError_t launch_conv1d_backward(const Conv1dParams &p, bool f32, bool vec, cudaStream_t s);
@@ -94,12 +114,12 @@ cudaError_t launch_conv1d_step(const Conv1dStepParams &p, bool f32, bool vec, cu
 int conv1d_strip(int rows, int C, int K, int sms);
 int conv1d_channels_per_block(int K);
 
-cudaError_t launch_rec_init(const RecParams &p, size_t words, float *carry, size_t carry_words, cudaStream_t s);
-cudaError_t launch_rec_forward(const RecParams &p, bool f32, bool vec, int sms, cudaStream_t s);
-cudaError_t launch_rec_backward(const RecParams &p, bool f32, bool vec, int sms, cudaStream_t s);
+cudaError_t launch_rec_init(const RecParams &p, size_t words, float *rates, cudaStream_t s);
+cudaError_t launch_rec_plain(const RecParams &p, bool f32, bool back, cudaStream_t s);
+cudaError_t launch_rec_tiles(const RecTiles &q, bool f32, bool back, cudaStream_t s);
 cudaError_t launch_rec_decay(const float *partial, const float *decay, float kappa, float *d_decay, int chunks, int C,
                              int Cpad, cudaStream_t s);
-cudaError_t launch_rec_step(const RecStepParams &p, bool f32, bool vec, cudaStream_t s);
+cudaError_t launch_rec_step(const RecStepParams &p, bool f32, cudaStream_t s);
 
 #ifdef __CUDACC__
 
@@ -127,14 +147,18 @@ __device__ __forceinline__ int seq_of(const Sequences &q, int row) {
     return lo;
 }
 
-// Whether the offsets begin at 0, never fall and end inside the rows.  Called by all threads
-// of one block; a violation is reported through the status word.
-__device__ __forceinline__ void check_offsets(const Sequences &q, int *status) {
+// Whether the offsets begin at 0, never fall and end inside the rows: looked at by `count` threads,
+// of which this is number `i`.  A violation is reported through the status word.
+__device__ __forceinline__ void check_offsets(const Sequences &q, int *status, int i, int count) {
     if (!q.offsets) return;
-    for (int s = threadIdx.x; s <= q.nseq; s += blockDim.x) {
+    for (int s = i; s <= q.nseq; s += count) {
         const int v = q.offsets[s], before = s ? q.offsets[s - 1] : 0;
         if (v < before || v > q.rows || (s == 0 && v != 0)) atomicExch(status, kDevBadOffsets);
     }
+}
+
+__device__ __forceinline__ void check_offsets(const Sequences &q, int *status) {
+    check_offsets(q, status, threadIdx.x, blockDim.x);
 }
 
 // Whether an earlier row of the batch names the same slot.  Called by all threads of a block.
@@ -157,6 +181,12 @@ __device__ __forceinline__ float rcp_approx(float x) {
 __device__ __forceinline__ float rsqrt_approx(float x) {
     float y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float sqrt_approx(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 

@@ -96,43 +96,84 @@ long long conv_row_blocks(long long rows, int C, int K, int sms, int *strip) {
     return ceil_div(rows, static_cast<long long>(*strip) * kConvWarps);
 }
 
-// The recurrence's scratch: [counter][aggregates][carries][decay sums], each at a multiple of 256 bytes.
+// The recurrence's scratch: [counter][aggregates][carries][decay rates][decay sums], each at a multiple of 256 bytes.
 struct RecLayout {
-    int chunks, tiles, Cpad;
-    size_t aggregate, carry, decay, forward_total, backward_total;
+    int chunks, per_seq, tiles, Cpad, chunk_rows;
+    size_t aggregate, carry, rates, decay, forward_total, backward_total;
 };
 
-int rec_layout(long long rows, int C, RecLayout *r) {
+// nseq = 0: the largest layout that these rows can need.
+constexpr int kOwnRows = 16 * 128;  // 16 of the largest chunks
+
+int rec_layout(const int *offsets, int nseq, int T, long long rows, int C, conv_dtype_t dtype, bool back, RecLayout *r) {
+    const int elt = elt_bytes(dtype);
+    if (elt == 0) return abi_fail(CONV_ERR_INVALID_ARG, "dtype must be CONV_F32 or CONV_BF16");
     if (rows < 0 || C < 1) return abi_fail(CONV_ERR_INVALID_ARG, "rows must be at least 0 and C at least 1");
     if (rows > kMaxRows) return abi_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows");
-    const long long chunks = rows ? ceil_div(rows, kRecChunk) : 1, tiles = ceil_div(C, kRecTile);
+    const long long chunk_rows = rec_shape(elt, back).rows(), tiles = ceil_div(C, kRecTile);
+    // Sequences of kOwnRows rows and more have chunks of their own; in shorter ones the last chunks, filled by half on the
+    // average, would cost more than the waiting that this saves.  That makes at most a 16th more chunks than the rows have.
+    const bool own = !offsets && nseq > 1 && T >= kOwnRows;
+    r->per_seq = own ? static_cast<int>(ceil_div(T, chunk_rows)) : 0;
+    long long chunks = rows ? ceil_div(rows, chunk_rows) : 1;
+    if (own) chunks = static_cast<long long>(r->per_seq) * nseq;
+    else if (nseq == 0) chunks += chunks / 16;
     if (chunks * tiles > kMaxBlocks) return abi_fail(CONV_ERR_UNSUPPORTED, "too many rows and channels for one launch");
     r->chunks = static_cast<int>(chunks);
     r->tiles = static_cast<int>(tiles);
+    r->chunk_rows = static_cast<int>(chunk_rows);
     r->Cpad = r->tiles * kRecTile;
     const size_t each = static_cast<size_t>(chunks) * r->Cpad * 4;  // a multiple of 256
     const bool joins = chunks > 1;
     r->aggregate = joins ? 256 : 0;
     r->carry = r->aggregate + (joins ? 2 * each : 0);
-    r->forward_total = r->carry + (joins ? each : 0);
+    r->rates = r->carry + (joins ? each : 0);
+    r->forward_total = r->rates + (joins ? static_cast<size_t>(r->Cpad) * 4 : 0);
     r->decay = r->forward_total;
     r->backward_total = r->decay + each;
     return CONV_OK;
 }
 
 // Points p into the scratch and fills the words that are their own flags.
-int rec_begin(RecParams *p, const RecLayout &r, void *workspace, float *saved, cudaStream_t stream) {
+int rec_begin(RecParams *p, const RecLayout &r, void *workspace, cudaStream_t stream) {
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p->chunks = r.chunks;
+    p->per_seq = r.per_seq;
     p->tiles = r.tiles;
     p->Cpad = r.Cpad;
     if (r.chunks == 1) return CONV_OK;
     p->ticket = reinterpret_cast<unsigned *>(ws);
     p->aggregate = reinterpret_cast<float2 *>(ws + r.aggregate);
-    p->carry = saved ? saved : reinterpret_cast<float *>(ws + r.carry);
-    const size_t each = static_cast<size_t>(r.chunks) * r.Cpad;
-    return abi_launch(launch_rec_init(*p, (saved ? r.carry : r.forward_total) / 4, saved, saved ? each : 0, stream),
-                      "recurrence scratch");
+    p->carry = reinterpret_cast<float *>(ws + r.carry);
+    float *rates = reinterpret_cast<float *>(ws + r.rates);
+    p->rates = rates;
+    return abi_launch(launch_rec_init(*p, r.rates / 4, rates, stream), "recurrence scratch");
+}
+
+// A tensor over rows as a tensor map of {C, rows}, boxes of kRecTile x box_rows; false where TMA does not take it.
+bool tile_map(const void *ptr, long long stride, long long rows, int C, int elt, int box_rows, CUtensorMap *map) {
+    const long long bytes = stride * elt;
+    if (rows < 1 || stride < C || bytes % 16 || bytes >= 1LL << 40 || !aligned(ptr, 16)) return false;
+    return abi_tensor_map_2d(map, ptr, elt, C, rows, bytes, kRecTile, box_rows) == CONV_OK;
+}
+
+// Runs the recurrence: in tiles where TMA takes every tensor, element by element otherwise.
+int run_rec(const RecParams &p, const RecLayout &r, int elt, bool back, cudaStream_t s) {
+    RecTiles q{};
+    const long long rows = p.seq.rows;
+    const int run = rec_shape(elt, back).run, chunk = r.chunk_rows;
+    bool tiles = tile_map(p.x, p.ldx, rows, p.C, elt, chunk, &q.in[0]) &&
+                 tile_map(p.ga, p.lda, rows, p.C, elt, chunk, &q.in[1]) &&
+                 tile_map(p.gx, p.ldg, rows, p.C, elt, chunk, &q.in[2]) &&
+                 tile_map(p.y, p.ldy, rows, p.C, elt, run, &q.out[0]);
+    if (back)
+        tiles = tiles && tile_map(p.dy, p.lddy, rows, p.C, elt, chunk, &q.in[3]) &&
+                tile_map(p.dga, p.ld_da, rows, p.C, elt, run, &q.out[1]) &&
+                tile_map(p.dgx, p.ld_dg, rows, p.C, elt, run, &q.out[2]);
+    const char *what = back ? "recurrence gradient" : "recurrence";
+    if (!tiles) return abi_launch(launch_rec_plain(p, elt == 4, back, s), what);
+    q.p = p;
+    return abi_launch(launch_rec_tiles(q, elt == 4, back, s), what);
 }
 
 int check_rec(const float *decay, float kappa) {
@@ -270,26 +311,28 @@ int conv1d_causal_step(const void *x, const void *w, const void *bias, void *y, 
     return abi_ok();
 }
 
-int gated_recurrence_saved_size(long long rows, int C, size_t *bytes) {
+int gated_recurrence_saved_size(long long rows, int C, conv_dtype_t dtype, size_t *bytes) {
     RecLayout r;
     if (!bytes) return abi_fail(CONV_ERR_INVALID_ARG, "bytes must not be NULL");
-    RETURN_IF(rec_layout(rows, C, &r));
-    *bytes = static_cast<size_t>(r.chunks) * r.Cpad * sizeof(float);
+    RETURN_IF(rec_layout(nullptr, 0, 0, rows, C, dtype, true, &r));
+    // one for every kRecRun rows; up to a chunk behind the last row, and behind each sequence that has chunks of its own
+    const size_t states = static_cast<size_t>(ceil_div(rows, kRecRun)) + (rows / kOwnRows + 1) * (kRecSavedSpare + 1);
+    *bytes = states * r.Cpad * sizeof(float);
     return abi_ok();
 }
 
-int gated_recurrence_workspace_size(long long rows, int C, size_t *bytes) {
+int gated_recurrence_workspace_size(long long rows, int C, conv_dtype_t dtype, size_t *bytes) {
     RecLayout r;
     if (!bytes) return abi_fail(CONV_ERR_INVALID_ARG, "bytes must not be NULL");
-    RETURN_IF(rec_layout(rows, C, &r));
+    RETURN_IF(rec_layout(nullptr, 0, 0, rows, C, dtype, false, &r));
     *bytes = r.forward_total;
     return abi_ok();
 }
 
-int gated_recurrence_backward_workspace_size(long long rows, int C, size_t *bytes) {
+int gated_recurrence_backward_workspace_size(long long rows, int C, conv_dtype_t dtype, size_t *bytes) {
     RecLayout r;
     if (!bytes) return abi_fail(CONV_ERR_INVALID_ARG, "bytes must not be NULL");
-    RETURN_IF(rec_layout(rows, C, &r));
+    RETURN_IF(rec_layout(nullptr, 0, 0, rows, C, dtype, true, &r));
     *bytes = r.backward_total;
     return abi_ok();
 }
@@ -310,19 +353,19 @@ int gated_recurrence_forward(const void *x, const void *gate_a, const void *gate
     RETURN_IF(check_state("state", state, "y", y, 4));
     RETURN_IF(check_state("saved", saved, "final_state", final_state, 16));
     RecLayout r;
-    RETURN_IF(rec_layout(rows, C, &r));
+    RETURN_IF(rec_layout(offsets, nseq, T, rows, C, dtype, false, &r));
     RETURN_IF(check_workspace(workspace, workspace_bytes, r.forward_total));
     AbiDevice dev;
     RETURN_IF(abi_device(&dev));
     RecParams p{};
     p.x = x; p.ga = gate_a; p.gx = gate_x; p.decay = decay; p.kappa = kappa; p.y = y;
-    p.state = state; p.final_state = final_state;
+    p.state = state; p.final_state = final_state; p.saved = static_cast<float *>(saved);
     p.ldx = x_stride; p.lda = gate_a_stride; p.ldg = gate_x_stride; p.ldy = y_stride;
     p.seq = Sequences{offsets, nseq, T, static_cast<int>(rows)};
     p.C = C; p.status = dev.status; p.timeout_ns = dev.timeout_ns; p.starve = dev.starve;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    RETURN_IF(rec_begin(&p, r, workspace, static_cast<float *>(saved), s));
-    RETURN_IF(abi_launch(launch_rec_forward(p, elt == 4, wide, dev.sms, s), "recurrence"));
+    RETURN_IF(rec_begin(&p, r, workspace, s));
+    RETURN_IF(run_rec(p, r, elt, false, s));
     return abi_ok();
 }
 
@@ -348,7 +391,7 @@ int gated_recurrence_backward(const void *x, const void *gate_a, const void *gat
     RETURN_IF(check_state("saved", saved, "d_state", d_state, 16));
     RETURN_IF(check_state("d_decay", d_decay, "decay", decay, 4));
     RecLayout r;
-    RETURN_IF(rec_layout(rows, C, &r));
+    RETURN_IF(rec_layout(offsets, nseq, T, rows, C, dtype, true, &r));
     RETURN_IF(check_workspace(workspace, workspace_bytes, r.backward_total));
     AbiDevice dev;
     RETURN_IF(abi_device(&dev));
@@ -356,15 +399,15 @@ int gated_recurrence_backward(const void *x, const void *gate_a, const void *gat
     p.x = x; p.ga = gate_a; p.gx = gate_x; p.dy = dy; p.decay = decay; p.kappa = kappa;
     p.y = dx; p.dga = d_gate_a; p.dgx = d_gate_x;
     p.state = state; p.d_final = d_final_state; p.d_state = d_state;
-    p.saved = static_cast<const float *>(saved);
+    p.saved = static_cast<float *>(const_cast<void *>(saved));  // only read
     p.decay_partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + r.decay);
     p.ldx = x_stride; p.lda = gate_a_stride; p.ldg = gate_x_stride; p.lddy = dy_stride;
     p.ldy = dx_stride; p.ld_da = d_gate_a_stride; p.ld_dg = d_gate_x_stride;
     p.seq = Sequences{offsets, nseq, T, static_cast<int>(rows)};
     p.C = C; p.status = dev.status; p.timeout_ns = dev.timeout_ns; p.starve = dev.starve;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    RETURN_IF(rec_begin(&p, r, workspace, nullptr, s));
-    RETURN_IF(abi_launch(launch_rec_backward(p, elt == 4, wide, dev.sms, s), "recurrence gradient"));
+    RETURN_IF(rec_begin(&p, r, workspace, s));
+    RETURN_IF(run_rec(p, r, elt, true, s));
     RETURN_IF(abi_launch(launch_rec_decay(p.decay_partial, decay, kappa, d_decay, p.chunks, C, p.Cpad, s),
                          "decay gradient sum"));
     return abi_ok();
@@ -397,7 +440,7 @@ int gated_recurrence_step(const void *x, const void *gate_a, const void *gate_x,
     p.tiles = static_cast<int>(ceil_div(C, 4 * kRecTile));
     if (static_cast<long long>(p.tiles) * B > kMaxBlocks)
         return abi_fail(CONV_ERR_UNSUPPORTED, "too many rows and channels for one launch");
-    RETURN_IF(abi_launch(launch_rec_step(p, elt == 4, wide, reinterpret_cast<cudaStream_t>(stream)), "recurrence step"));
+    RETURN_IF(abi_launch(launch_rec_step(p, elt == 4, reinterpret_cast<cudaStream_t>(stream)), "recurrence step"));
     return abi_ok();
 }
 

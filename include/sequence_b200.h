@@ -83,12 +83,13 @@ int conv1d_causal_step(const void *x, const void *w, const void *bias, void *y, 
  * 1e-37 (gate_a of the lowest value, or -infinity) the row keeps the state and adds
  * 0 * rx * x.  kappa: finite and above 0. */
 
-/* Bytes of the states that the forward pass saves for the backward pass (opaque). */
-int gated_recurrence_saved_size(long long rows, int C, size_t *bytes);
+/* Bytes of the states that the forward pass saves for the backward pass (opaque): an fp32 state
+ * for every 8 rows, an eighth of the bytes of y in fp32 and a quarter in bf16. */
+int gated_recurrence_saved_size(long long rows, int C, conv_dtype_t dtype, size_t *bytes);
 
 /* Device scratch bytes of the forward pass, and of the backward pass. */
-int gated_recurrence_workspace_size(long long rows, int C, size_t *bytes);
-int gated_recurrence_backward_workspace_size(long long rows, int C, size_t *bytes);
+int gated_recurrence_workspace_size(long long rows, int C, conv_dtype_t dtype, size_t *bytes);
+int gated_recurrence_backward_workspace_size(long long rows, int C, conv_dtype_t dtype, size_t *bytes);
 
 /* The forward pass: y = h.
  *   state, final_state : (nseq, C) fp32, or NULL; final_state receives the last h of each

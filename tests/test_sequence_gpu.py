@@ -43,15 +43,17 @@ def shape_of(B, T, C, offsets, rows):
 CASES = [  # B, T, offsets, rows (behind the last sequence), C, K, silu, carried state
     (1, 1, None, None, 1, 2, True, False),
     (2, 3, None, None, 5, 8, True, True),           # sequences shorter than the window
-    (3, 130, None, None, 66, 4, True, True),        # a chunk of the recurrence and 2 rows; ragged channels
+    (3, 130, None, None, 66, 4, True, True),        # chunks of the recurrence across sequences; ragged channels
     (1, 300, None, None, 130, 3, False, False),
-    (2, 128, None, None, 128, 4, True, True),       # whole chunks, wide accesses
+    (2, 128, None, None, 128, 4, True, True),       # wide accesses
     (2, 257, None, None, 40, 6, True, True),
     (1, 0, None, None, 8, 4, True, True),           # no rows
-    (1, 2100, None, None, 4, 4, True, True),        # a carry over 17 chunks
+    (3, 56, None, None, 24, 2, False, True),        # sequences that end with their chunks
+    (1, 2100, None, None, 4, 4, True, True),        # a carry over many chunks
+    (2, 2050, None, None, 16, 3, False, True),      # sequences with chunks of their own
     (5, 0, [0, 0, 1, 1, 140, 141], None, 72, 4, True, True),
     (4, 0, [0, 7, 7, 300, 300], 333, 64, 5, False, True),   # empty ones, and rows of no sequence
-    (3, 0, [0, 128, 256, 384], 384, 64, 4, True, False),    # sequences that end with their chunks
+    (3, 0, [0, 128, 256, 384], 384, 64, 4, True, False),    # ... that end at multiples of runs
     (40, 0, list(range(0, 123, 3)), 122, 33, 7, True, True),  # many short ones
     (2, 0, [0, 0, 0], 9, 16, 4, True, True),        # rows, but none of a sequence
 ]

@@ -15,6 +15,9 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 TABLES = {"sequence_b200.h": sequence.SIGNATURES, "optimizer_b200.h": optimizer.SIGNATURES}
 
 
+BF, F = cb.CONV_BF16, cb.CONV_F32
+
+
 @pytest.fixture(scope="module")
 def lib():
     from cnn_convolution_conv2d_b200 import build
@@ -43,24 +46,28 @@ def test_sizes(lib):
     # without a device strips are 64 rows, four to a block: 1000 rows are 4 blocks of (K + 1) C sums
     if not torch.cuda.is_available():
         assert cb.conv1d_causal_backward_workspace_size(1000, 64, 4) == 4 * 5 * 64 * 4
-    # one chunk: nothing to join; a state for each chunk and channel (rounded up to 64) otherwise
-    assert cb.gated_recurrence_workspace_size(128, 100) == 0
-    assert cb.gated_recurrence_saved_size(129, 100) == 2 * 128 * 4
-    assert cb.gated_recurrence_workspace_size(129, 100) == 256 + 2 * 128 * 12
-    assert cb.gated_recurrence_backward_workspace_size(129, 100) == 256 + 2 * 128 * 16
-    for bad in ((-1, 4), (5, 0)):
+    # one chunk (forward 128 rows in bf16, 64 in fp32; backward 56 and 48): nothing to join; otherwise three values for
+    # each chunk and channel (rounded up to 64), and a rate; backward also a sum for each
+    assert cb.gated_recurrence_workspace_size(128, 100, BF) == 0 and cb.gated_recurrence_workspace_size(64, 100, F) == 0
+    assert cb.gated_recurrence_workspace_size(129, 100, BF) == 256 + 2 * 128 * 12 + 128 * 4
+    assert cb.gated_recurrence_workspace_size(129, 100, F) == 256 + 3 * 128 * 12 + 128 * 4
+    assert cb.gated_recurrence_backward_workspace_size(56, 100, BF) == 128 * 4
+    assert cb.gated_recurrence_backward_workspace_size(57, 100, BF) == 256 + 2 * 128 * 16 + 128 * 4
+    assert cb.gated_recurrence_backward_workspace_size(49, 100, F) == 256 + 2 * 128 * 16 + 128 * 4
+    # a saved state for every 8 rows, and room for those of the rows behind the last one in its chunk
+    assert cb.gated_recurrence_saved_size(129, 100, BF) == cb.gated_recurrence_saved_size(129, 100, F) == (17 + 33) * 128 * 4
+    for bad in ((-1, 4, BF), (5, 0, BF), (5, 4, 7)):
         with pytest.raises(cb.Conv2dError) as err:
             cb.gated_recurrence_saved_size(*bad)
         assert err.value.status == cb.CONV_ERR_INVALID_ARG
     with pytest.raises(cb.Conv2dError) as err:
-        cb.gated_recurrence_workspace_size(2 ** 31, 4)
+        cb.gated_recurrence_workspace_size(2 ** 31, 4, BF)
     assert err.value.status == cb.CONV_ERR_UNSUPPORTED
     for K in (1, 9):
         with pytest.raises(cb.Conv2dError):
             cb.conv1d_causal_backward_workspace_size(8, 8, K)
 
 
-BF, F = cb.CONV_BF16, cb.CONV_F32
 INVALID, UNSUPPORTED = cb.CONV_ERR_INVALID_ARG, cb.CONV_ERR_UNSUPPORTED
 
 
