@@ -3,10 +3,13 @@
 //   g = grad scale, m = b1 m + (1-b1) g, v = b2 v + (1-b2) g^2,
 //   p = p (1 - lr wd) - lr m / (1-b1^t) / (sqrt(v / (1-b2^t)) + eps)
 //
-// Bound by HBM: about 15 operations (8-bit states: about 60) for 10 to 28 bytes an element, each
-// read and written once.  A block takes 2048 elements of one tensor, found by a search in the
-// table of tensors, which is a kernel argument: nothing is uploaded, and a captured launch keeps
-// its own copy.
+// With 32-bit states bound by HBM (28 bytes an element, 6.6 TB/s); with 8-bit states by the issue of
+// instructions, about 70 for an element's 10 bytes: a third of them the random bits and the rounding.  So there a thread
+// keeps to 40 registers, for 48 warps an SM, and a block takes several batches of 1024 elements of one tensor, which it
+// finds by a search in the table of tensors.  The table is a kernel argument: nothing is uploaded, and a captured
+// launch keeps its own copy.  Every element is read and written once.
+// 100 M elements: fp32 420 us (6.7 TB/s); bf16 with fp32 master weights 420 us, with 8-bit states 258 us (3.9 TB/s),
+// with both 297 us (5.4 TB/s).
 //
 // 8-bit states hold 256 elements (a warp's) to one scale, a power of two, so that scaling is
 // exact: m in e4m3 (largest element in [2^7, 2^8)), v in e5m2 ([2^14, 2^15): v spans twice the
@@ -25,6 +28,17 @@ namespace conv2d_b200 {
 namespace {
 
 constexpr int E = kAdamPerThread;
+
+__device__ __forceinline__ float sqrt_approx(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 template <typename T>
 __device__ __forceinline__ void load8(float (&f)[E], const T *p, int valid) {
@@ -101,33 +115,27 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t h) {
 
 __device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7fffffffu) < 0x7f800000u; }
 
-// The block's scale: a power of two that brings the largest finite |value| of the warp into [2^kTop, 2^(kTop+1)).
+__device__ __forceinline__ uint32_t size_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// The scale of a warp's values from the bits of the largest size: a power of two that brings it into
+// [2^kTop, 2^(kTop+1)).
 template <int kTop>
-__device__ __forceinline__ float warp_scale(const float (&f)[E], float &inverse) {
-    uint32_t big = 0;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const uint32_t b = __float_as_uint(f[i]) & 0x7fffffffu;
-        big = max(big, b < 0x7f800000u ? b : 0u);
-    }
-    big = __reduce_max_sync(0xffffffffu, big);
-    inverse = 1.f;
-    if (big == 0) return 1.f;
+__device__ __forceinline__ float scale_of(uint32_t big, float &inverse) {
     const uint32_t e = max(big >> 23, static_cast<uint32_t>(kTop + 1)) - kTop;
-    inverse = __uint_as_float((254u - e) << 23);
-    return __uint_as_float(e << 23);
+    inverse = big ? __uint_as_float((254u - e) << 23) : 1.f;
+    return big ? __uint_as_float(e << 23) : 1.f;
 }
 
-// Rounds v (already scaled) to kKeep fraction bits, up where the random bits carry.  Below 2^kSmall, the smallest
-// normal number, the steps stay equal: there v is rounded one binade higher and brought back.
-template <int kSmall, int kKeep>
+// Rounds v (already scaled) to kKeep fraction bits, up where the random bits carry: the lowest of them weighs
+// 2^-16 of a step.  Below 2^kSmall, the smallest normal number, the steps stay equal: there v is rounded one binade higher
+// and brought back.  (The bits of a float grow with its size whatever its sign.)
+template <int kSmall, int kKeep, bool kSigned>
 __device__ __forceinline__ float round_by_chance(float v, uint32_t bits16) {
     constexpr float kLift = kSmall == -6 ? 0x1p-6f : 0x1p-14f;
     constexpr int kLow = 23 - kKeep;
-    const float size = fabsf(v);
-    const float lift = size < kLift ? kLift : 0.f;
-    const uint32_t whole = __float_as_uint(__fadd_rn(size, lift)) + (bits16 << (kLow - 16));
-    return copysignf(__uint_as_float(whole >> kLow << kLow) - lift, v);
+    const float lift = fabsf(v) < kLift ? (kSigned ? copysignf(kLift, v) : kLift) : 0.f;
+    const uint32_t whole = __float_as_uint(__fadd_rn(v, lift)) + bits16 * (1u << (kLow - 16));
+    return __uint_as_float(whole & ~((1u << kLow) - 1u)) - lift;
 }
 
 template <__nv_fp8_interpretation_t kKind>
@@ -148,7 +156,7 @@ __device__ __forceinline__ void store_codes(uint8_t *p, const float (&f)[E], int
 }
 
 template <typename P, typename G, bool kMaster, bool kEight>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamParams q) {
+__global__ void __launch_bounds__(kAdamThreads, kEight ? 12 : 1) adamw_kernel(const __grid_constant__ AdamParams q) {
     __shared__ float s_rate[2];
     float rate = q.rate, root = q.root;
     long long step = q.step;
@@ -170,53 +178,84 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
         if (q.first[mid] <= blockIdx.x) lo = mid; else hi = mid - 1;
     }
     const AdamTensor &t = q.t[lo];
-    const long long at = static_cast<long long>(blockIdx.x - q.first[lo]) * kAdamPerBlock + threadIdx.x * E;
-    const int valid = at >= t.n ? 0 : t.n - at < E ? static_cast<int>(t.n - at) : E;
-    float g[E], m[E], v[E], w[E];
-    load8(g, static_cast<const G *>(t.g) + at, valid);
-    if constexpr (kMaster) load8(w, t.master + at, valid);
-    else load8(w, static_cast<const P *>(t.p) + at, valid);
-    const long long quant = at / kAdamQuant;   // the same for the lanes of a warp
-    const bool any = quant * kAdamQuant < t.n;
-    if constexpr (kEight) {
-        load_codes<__NV_E4M3>(m, static_cast<const uint8_t *>(t.m) + at, any ? t.m_scale[quant] : 1.f, valid);
-        load_codes<__NV_E5M2>(v, static_cast<const uint8_t *>(t.v) + at, any ? t.v_scale[quant] : 1.f, valid);
-    } else {
-        load8(m, static_cast<const float *>(t.m) + at, valid);
-        load8(v, static_cast<const float *>(t.v) + at, valid);
-    }
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const float gs = g[i] * scale;
-        // each product rounded by itself: the 8-bit codes below are a fixed function of the inputs
-        m[i] = __fadd_rn(__fmul_rn(m[i], q.beta1), __fmul_rn(gs, q.beta1c));
-        v[i] = __fadd_rn(__fmul_rn(v[i], q.beta2), __fmul_rn(__fmul_rn(gs, gs), q.beta2c));
-        const float denom = fmaf(sqrtf(v[i]), root, q.eps);
-        w[i] = fmaf(w[i], q.keep, -rate * __fdividef(m[i], denom));
-    }
-    if constexpr (kMaster) store8(t.master + at, w, valid);
-    store8(static_cast<P *>(t.p) + at, w, valid);
-    if constexpr (kEight) {
-        float im, iv;
-        const float sm = warp_scale<7>(m, im), sv = warp_scale<14>(v, iv);
-        const uint32_t key = mix(mix(q.seed + 0x9E3779B9u * static_cast<uint32_t>(step)) + 0x85EBCA77u * (q.index0 + lo + 1));
+    const uint32_t key = kEight ? mix(mix(q.seed + 0x9E3779B9u * static_cast<uint32_t>(step)) + 0x85EBCA77u * (q.index0 + lo + 1)) : 0u;
+    const float minus_rate = -rate;
+    long long at = static_cast<long long>(blockIdx.x - q.first[lo]) * q.batches * kAdamBatch + threadIdx.x * E;
+    for (int batch = 0; batch < q.batches; ++batch, at += kAdamBatch) {
+        const long long quant = at / kAdamQuant;   // the same for the lanes of a warp
+        if (quant * kAdamQuant >= t.n) return;
+        const int valid = at >= t.n ? 0 : t.n - at < E ? static_cast<int>(t.n - at) : E;
+        float g[E], m[E], v[E], w[E];
+        load8(g, static_cast<const G *>(t.g) + at, valid);
+        if constexpr (kMaster) load8(w, t.master + at, valid);
+        else load8(w, static_cast<const P *>(t.p) + at, valid);
+        if constexpr (kEight) {
+            load_codes<__NV_E4M3>(m, static_cast<const uint8_t *>(t.m) + at, t.m_scale[quant], valid);
+            load_codes<__NV_E5M2>(v, static_cast<const uint8_t *>(t.v) + at, t.v_scale[quant], valid);
+        } else {
+            load8(m, static_cast<const float *>(t.m) + at, valid);
+            load8(v, static_cast<const float *>(t.v) + at, valid);
+        }
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            const uint32_t h = mix(static_cast<uint32_t>(at + i) * 0x9E3779B1u + key);
-            const float cm = round_by_chance<-6, 3>(m[i] * im, h & 0xffffu);
-            const float cv = round_by_chance<-14, 2>(v[i] * iv, h >> 16);
-            m[i] = finite(m[i]) ? cm : __int_as_float(0x7fc00000);
-            v[i] = !finite(v[i]) ? __int_as_float(0x7fc00000) : v[i] > 0.f ? fmaxf(cv, 0x1p-16f) : cv;
+            const float gs = g[i] * scale;
+            // each product rounded by itself: the 8-bit codes below are a fixed function of the inputs
+            m[i] = __fadd_rn(__fmul_rn(m[i], q.beta1), __fmul_rn(gs, q.beta1c));
+            v[i] = __fadd_rn(__fmul_rn(v[i], q.beta2), __fmul_rn(__fmul_rn(gs, gs), q.beta2c));
+            // (the root and the quotient are off by a few units of an update that is a thousandth of the weight or less)
+            w[i] = fmaf(w[i], q.keep, minus_rate * (m[i] * rcp_approx(fmaf(sqrt_approx(v[i]), root, q.eps))));
         }
-        store_codes<__NV_E4M3>(static_cast<uint8_t *>(t.m) + at, m, valid);
-        store_codes<__NV_E5M2>(static_cast<uint8_t *>(t.v) + at, v, valid);
-        if ((threadIdx.x & 31) == 0 && any) {
-            t.m_scale[quant] = sm;
-            t.v_scale[quant] = sv;
+        if constexpr (kMaster) store8(t.master + at, w, valid);
+        store8(static_cast<P *>(t.p) + at, w, valid);
+        if constexpr (kEight) {
+            uint32_t big_m = 0, big_v = 0;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                big_m = max(big_m, size_bits(m[i]));
+                big_v = max(big_v, __float_as_uint(v[i]));  // v has no sign
+            }
+            big_m = __reduce_max_sync(0xffffffffu, big_m);
+            big_v = __reduce_max_sync(0xffffffffu, big_v);
+            // Elements that are not finite: they are held as NaN and leave the scale to the others.  Rare, and the warp's own.
+            uint32_t lost_m = 0, lost_v = 0;
+            if (big_m >= 0x7f800000u || big_v >= 0x7f800000u) {
+                big_m = big_v = 0;
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    if (finite(m[i])) big_m = max(big_m, size_bits(m[i])); else lost_m |= 1u << i;
+                    if (finite(v[i])) big_v = max(big_v, size_bits(v[i])); else lost_v |= 1u << i;
+                }
+                big_m = __reduce_max_sync(0xffffffffu, big_m);
+                big_v = __reduce_max_sync(0xffffffffu, big_v);
+            }
+            float im, iv;
+            const float scale_m = scale_of<7>(big_m, im), scale_v = scale_of<14>(big_v, iv);
+            const uint32_t first = static_cast<uint32_t>(at) * 0x9E3779B1u + key;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const uint32_t h = mix(first + i * 0x9E3779B1u);
+                m[i] = round_by_chance<-6, 3, true>(m[i] * im, h & 0xffffu);
+                const float sv = v[i] * iv;
+                // the smallest code where v is above zero (and not 2^-142 of the largest), else 0
+                v[i] = fmaxf(round_by_chance<-14, 2, false>(sv, h >> 16), fminf(sv * 0x1p126f, 0x1p-16f));
+            }
+            if (lost_m | lost_v) {
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    if (lost_m >> i & 1u) m[i] = __int_as_float(0x7fc00000);
+                    if (lost_v >> i & 1u) v[i] = __int_as_float(0x7fc00000);
+                }
+            }
+            store_codes<__NV_E4M3>(static_cast<uint8_t *>(t.m) + at, m, valid);
+            store_codes<__NV_E5M2>(static_cast<uint8_t *>(t.v) + at, v, valid);
+            if ((threadIdx.x & 31) == 0) {
+                t.m_scale[quant] = scale_m;
+                t.v_scale[quant] = scale_v;
+            }
+        } else {
+            store8(static_cast<float *>(t.m) + at, m, valid);
+            store8(static_cast<float *>(t.v) + at, v, valid);
         }
-    } else {
-        store8(static_cast<float *>(t.m) + at, m, valid);
-        store8(static_cast<float *>(t.v) + at, v, valid);
     }
 }
 

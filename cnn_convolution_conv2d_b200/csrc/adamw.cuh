@@ -6,10 +6,11 @@
 namespace conv2d_b200 {
 
 constexpr int kAdamTensors = 48;     // tensors of one launch: their table travels as a kernel argument
-constexpr int kAdamThreads = 256;
+constexpr int kAdamThreads = 128;
 constexpr int kAdamPerThread = 8;
 constexpr int kAdamQuant = 256;      // elements of one scale of an 8-bit state: a warp's
-constexpr int kAdamPerBlock = kAdamThreads * kAdamPerThread;
+constexpr int kAdamBatch = kAdamThreads * kAdamPerThread;  // elements that a block takes at a time
+constexpr int kAdamBatches = 8;      // batches of a block where there are enough elements
 
 struct AdamTensor {
     void *p;
@@ -24,6 +25,7 @@ struct AdamParams {
     AdamTensor t[kAdamTensors];
     unsigned first[kAdamTensors + 1];  // the first block of each tensor; [count]: all blocks
     int count;
+    int batches;                       // batches of a block
     unsigned index0;                   // the first tensor's place in the whole list
     float beta1, beta1c, beta2, beta2c;  // c: 1 - beta
     float keep;                        // 1 - lr * weight_decay
