@@ -13,6 +13,7 @@ from them, share none.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import _check, _dtype_code, load
 
@@ -45,34 +46,39 @@ def conv1d_causal_backward_workspace_size(rows, C, K) -> int:
     return _size(load().conv1d_causal_backward_workspace_size, rows, C, K)
 
 
+# These three depend on their arguments alone: asked once for each.
+@functools.lru_cache(maxsize=4096)
 def gated_recurrence_saved_size(rows, C, dtype) -> int:
     return _size(load().gated_recurrence_saved_size, rows, C, dtype)
 
 
+@functools.lru_cache(maxsize=4096)
 def gated_recurrence_workspace_size(rows, C, dtype) -> int:
     return _size(load().gated_recurrence_workspace_size, rows, C, dtype)
 
 
+@functools.lru_cache(maxsize=4096)
 def gated_recurrence_backward_workspace_size(rows, C, dtype) -> int:
     return _size(load().gated_recurrence_backward_workspace_size, rows, C, dtype)
 
 
 # ------------------------------------------------------------ argument checks ---
-def _rows(name, t, like, shape=None, dtype=None):
-    """(pointer, row stride) of a tensor over rows: on `like`'s device, of `like`'s shape and dtype
-    unless others are given."""
-    if t.device != like.device or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {like.device}, not on {t.device}")
-    if t.dtype != (dtype or like.dtype):
-        raise TypeError(f"{name} must be {dtype or like.dtype}, not {t.dtype}")
-    if t.shape != (shape or like.shape):
-        raise ValueError(f"{name} must have the shape {tuple(shape or like.shape)}, not {tuple(t.shape)}")
+def _rows(name, t, like):
+    """(pointer, row stride) of a tensor over rows: on `like`'s device, of `like`'s shape and dtype."""
+    if t is not like:
+        if t.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}, not on {t.device}")
+        if t.dtype != like.dtype:
+            raise TypeError(f"{name} must be {like.dtype}, not {t.dtype}")
+        if t.shape != like.shape:
+            raise ValueError(f"{name} must have the shape {tuple(like.shape)}, not {tuple(t.shape)}")
+    sizes = t.shape
     if t.is_contiguous():
-        return t.data_ptr(), t.shape[-1]
-    stride, sizes = t.stride(), t.shape
+        return t.data_ptr(), sizes[-1]
+    stride = t.stride()
     if sizes[-1] > 1 and stride[-1] != 1:
         raise ValueError(f"the channels of {name} must be contiguous")
-    if t.dim() == 2:
+    if len(sizes) == 2:
         return t.data_ptr(), stride[0] if sizes[0] > 1 else max(stride[0], sizes[1])
     B, T, C = sizes
     if T > 1:
@@ -80,6 +86,12 @@ def _rows(name, t, like, shape=None, dtype=None):
             raise ValueError(f"the rows of {name} must lie a fixed distance apart; use {name}.contiguous()")
         return t.data_ptr(), stride[1]
     return t.data_ptr(), stride[0] if B > 1 else max(stride[0], C)
+
+
+def _new(x):
+    """An uninitialised tensor like x, contiguous."""
+    import torch
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def _whole(name, t, shape, dtype, device):
@@ -112,14 +124,23 @@ def _sequences(x, offsets):
     return offsets.data_ptr(), offsets.numel() - 1, 0, x.shape[0], x.shape[1]
 
 
+def _current_stream(index):
+    """The handle of a device's current stream: without the stream object, whose making costs more than a launch, where
+    this torch offers that."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _on(x, stream, call):
     """call(raw stream) with x's device current, and `stream` (a torch stream or a handle) where
     one is given, so that what the call allocates belongs to the stream it is used on."""
     import torch
     if not x.is_cuda:
         raise ValueError("tensors passed to the library must be CUDA tensors")
-    if stream is None and torch.cuda.current_device() == x.device.index:
-        return call(torch.cuda.current_stream().cuda_stream)
+    index = x.device.index
+    if stream is None and torch.cuda.current_device() == index:
+        return call(_current_stream(index))
     with torch.cuda.device(x.device):
         if stream is None:
             return call(torch.cuda.current_stream().cuda_stream)
@@ -175,7 +196,6 @@ class CausalConv1dB200:
     def __call__(self, x, y=None, offsets=None, initial_state=None, final_state=None, stream=None):
         """y for x (B, T, C), or (rows, C) with offsets.  ``initial_state`` (B, K-1, C): the rows before each
         sequence; ``final_state``: a buffer of that shape that receives its last K-1 rows."""
-        import torch
         self._input(x)
         seq = _sequences(x, offsets)
         window = (seq[1], self.K - 1, self.C)
@@ -184,7 +204,7 @@ class CausalConv1dB200:
         final = _whole("final_state", final_state, window, x.dtype, x.device)
 
         def call(s):
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+            out = _new(x) if y is None else y
             py, ldy = _rows("y", out, x)
             _check(load().conv1d_causal_forward(px, self.w.data_ptr(), self._bias(), py, state, final, *seq, self.K,
                                                 self.act, ldx, ldy, self.dtype, s))
@@ -198,7 +218,6 @@ class CausalConv1dB200:
                  d_initial_state=None, stream=None):
         """(dx, dw, db, d_initial_state) for the forward pass's arguments and dy; db without a bias and
         d_initial_state without an initial state are None."""
-        import torch
         self._input(x)
         seq = _sequences(x, offsets)
         window = (seq[1], self.K - 1, self.C)
@@ -208,11 +227,10 @@ class CausalConv1dB200:
         dfinal = _whole("d_final_state", d_final_state, window, x.dtype, x.device)
 
         def call(s):
-            empty = lambda *shape: torch.empty(shape, dtype=x.dtype, device=x.device)  # noqa: E731
-            gx = empty(*x.shape) if dx is None else dx
-            gw = empty(self.C, self.K) if dw is None else dw
-            gb = empty(self.C) if db is None and self.bias is not None else db
-            gs = empty(*window) if d_initial_state is None and initial_state is not None else d_initial_state
+            gx = _new(x) if dx is None else dx
+            gw = _new(self.w) if dw is None else dw
+            gb = _new(self.bias) if db is None and self.bias is not None else db
+            gs = _new(initial_state) if d_initial_state is None and initial_state is not None else d_initial_state
             pgx, ldgx = _rows("dx", gx, x)
             ws = _scratch(conv1d_causal_backward_workspace_size(seq[3], self.C, self.K), x.device)
             _check(load().conv1d_causal_backward(
@@ -227,7 +245,6 @@ class CausalConv1dB200:
         """One token for each of B sequences: y (B, C) for x (B, C), and the windows in ``state`` (pool, K-1, C)
         moved on in place.  Row b's window is state[slots[b]] (int32; outside the pool: no sequence, y's row stays
         as it was), or state[b] without slots."""
-        import torch
         self._input(x)
         if x.dim() != 2:
             raise ValueError("x must be (B, C)")
@@ -237,7 +254,7 @@ class CausalConv1dB200:
         pslots = _slots(slots, B, x.device)
 
         def call(s):
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+            out = _new(x) if y is None else y
             py, ldy = _rows("y", out, x)
             _check(load().conv1d_causal_step(px, self.w.data_ptr(), self._bias(), py, ps, pslots, B, state.shape[0],
                                              self.C, self.K, self.act, ldx, ldy, self.dtype, s))
@@ -292,7 +309,7 @@ class GatedRecurrenceB200:
         psaved = None if saved is None else self._saved(saved, seq[3], code, x.device)
 
         def call(s):
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+            out = _new(x) if y is None else y
             py, ldy = _rows("y", out, x)
             ws = _scratch(gated_recurrence_workspace_size(seq[3], self.C, code), x.device)
             _check(load().gated_recurrence_forward(
@@ -316,12 +333,9 @@ class GatedRecurrenceB200:
         psaved = self._saved(saved, seq[3], code, x.device)
 
         def call(s):
-            like = lambda t: torch.empty(x.shape, dtype=x.dtype, device=x.device) if t is None else t  # noqa: E731
-            gx, ga, gg = like(dx), like(d_gate_a), like(d_gate_x)
-            gd = torch.empty(self.C, dtype=f32, device=x.device) if d_decay is None else d_decay
-            gs = d_initial_state
-            if gs is None and initial_state is not None:
-                gs = torch.empty(seq[1], self.C, dtype=f32, device=x.device)
+            gx, ga, gg = (_new(x) if t is None else t for t in (dx, d_gate_a, d_gate_x))
+            gd = _new(self.decay) if d_decay is None else d_decay
+            gs = _new(initial_state) if d_initial_state is None and initial_state is not None else d_initial_state
             (pgx, ldgx), (pga, ldga), (pgg, ldgg) = _rows("dx", gx, x), _rows("d_gate_a", ga, x), _rows("d_gate_x", gg, x)
             ws = _scratch(gated_recurrence_backward_workspace_size(seq[3], self.C, code), x.device)
             _check(load().gated_recurrence_backward(
@@ -345,7 +359,7 @@ class GatedRecurrenceB200:
         pslots = _slots(slots, B, x.device)
 
         def call(s):
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+            out = _new(x) if y is None else y
             py, ldy = _rows("y", out, x)
             _check(load().gated_recurrence_step(px, pa, pg, self.decay.data_ptr(), self.kappa, py, ps, pslots, B,
                                                 state.shape[0], self.C, ldx, lda, ldg, ldy, code, s))
