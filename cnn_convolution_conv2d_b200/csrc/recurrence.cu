@@ -453,8 +453,8 @@ __device__ __forceinline__ bool forward_item(const RecParams &p, Rows &rows, con
     float2 y = h;
 #pragma unroll
     for (int j = 0; j < L; ++j) {
-        if (j % kRecRun == 0 && p.saved) store2(p.saved + static_cast<size_t>(rows.saved + j / kRecRun) * p.Cpad, y, rows.l);
         if (kEdge && !(run.in >> j & 1u)) continue;
+        if (j % kRecRun == 0 && p.saved) store2(p.saved + static_cast<size_t>(rows.saved + j / kRecRun) * p.Cpad, y, rows.l);
         y = kEdge ? make_float2(after(A[j].x, H[j].x, h.x), after(A[j].y, H[j].y, h.y)) : fma2(A[j], h, H[j]);
         rows.put(0, j, y);
         if (kEdge && (run.end >> j & 1u) && p.final_state)
@@ -484,7 +484,8 @@ __device__ __forceinline__ bool backward_item(const RecParams &p, Rows &rows, co
                                               float2 (*s_sum)[32], int warp, Halfway halfway) {
     constexpr int L = Rows::kRun;
     static_assert(L == kRecRun, "a saved state for each run");
-    float2 h = load2<float>(p.saved + static_cast<size_t>(rows.saved) * p.Cpad, rows.l);
+    float2 h = splat(0.f);  // what enters the run
+    if (!kEdge || (run.in & 1u)) h = load2<float>(p.saved + static_cast<size_t>(rows.saved) * p.Cpad, rows.l);
     const float2 rate = decay_rate(p, rows.l);
     float2 pm[L], ra[L], rx[L], before[L];  // a - 1, the gates, h[t-1]
 #pragma unroll
@@ -596,7 +597,7 @@ __device__ __forceinline__ int chunk_limit(const RecParams &p, int chunk) {
 __device__ __forceinline__ int saved_place(const RecParams &p, int chunk, int row0) {
     if (!p.per_seq) return row0 / kRecRun;
     const int s = chunk / p.per_seq;
-    return s * ((p.seq.T + kRecRun - 1) / kRecRun + kRecSavedSpare) + (row0 - s * p.seq.T) / kRecRun;
+    return s * ((p.seq.T + kRecRun - 1) / kRecRun) + (row0 - s * p.seq.T) / kRecRun;
 }
 
 // An item.

@@ -95,7 +95,6 @@ struct RecStepParams {
 constexpr int kConvWarps = 4;     // warps of a conv1d block, one strip of rows each
 constexpr int kRecTile = 64;      // channels of a work item of the recurrence
 constexpr int kRecRun = 8;        // rows of one saved state
-constexpr int kRecSavedSpare = 32;  // saved states of rows behind a sequence's last one, in its last chunk
 
 // How a kernel of the recurrence is laid out: working warps, rows that one scans, stages of shared memory, blocks an SM.
 struct RecShape {

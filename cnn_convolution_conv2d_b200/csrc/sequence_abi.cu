@@ -1,5 +1,6 @@
 // sequence_abi.cu -- the C ABI declared in include/sequence_b200.h: argument validation, the
 // scratch layout and kernel dispatch.  Host code only.
+#include <algorithm>
 #include <cmath>
 
 #include "host.cuh"
@@ -102,22 +103,34 @@ struct RecLayout {
     size_t aggregate, carry, rates, decay, forward_total, backward_total;
 };
 
-// nseq = 0: the largest layout that these rows can need.
-constexpr int kOwnRows = 16 * 128;  // 16 of the largest chunks
+// Whether each of nseq sequences of T rows has chunks of its own, in both directions (they share the saved states):
+// then a chunk hardly ever waits for the one in front of it, but the last chunk of each sequence is not full.
+// Taken where that costs an eighth at most, or where there are few items, whose time is the waiting: there
+// up to half may be empty (3 x 777 rows of 1001 channels in fp32, forward and backward: 75 -> XX us).
+bool own_chunks(int nseq, int T, long long tiles, int elt) {
+    if (T < 1) return false;
+    bool full = true, few = true;
+    for (const bool back : {false, true}) {
+        const long long chunk_rows = rec_shape(elt, back).rows(), per_seq = ceil_div(T, chunk_rows);
+        full = full && 8 * per_seq * chunk_rows <= 9LL * T;
+        few = few && per_seq * chunk_rows <= 2LL * T && per_seq * nseq * tiles <= 4 * 296;
+    }
+    return full || few;
+}
 
-int rec_layout(const int *offsets, int nseq, int T, long long rows, int C, conv_dtype_t dtype, bool back, RecLayout *r) {
+// T = 0: packed sequences.
+int rec_layout(int nseq, int T, long long rows, int C, conv_dtype_t dtype, bool back, RecLayout *r) {
     const int elt = elt_bytes(dtype);
     if (elt == 0) return abi_fail(CONV_ERR_INVALID_ARG, "dtype must be CONV_F32 or CONV_BF16");
-    if (rows < 0 || C < 1) return abi_fail(CONV_ERR_INVALID_ARG, "rows must be at least 0 and C at least 1");
+    if (nseq < 1 || T < 0 || rows < 0 || C < 1)
+        return abi_fail(CONV_ERR_INVALID_ARG, "nseq and C must be at least 1, T and rows at least 0");
+    if (T > 0 && rows != static_cast<long long>(nseq) * T) return abi_fail(CONV_ERR_INVALID_ARG, "rows must be nseq * T");
     if (rows > kMaxRows) return abi_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows");
     const long long chunk_rows = rec_shape(elt, back).rows(), tiles = ceil_div(C, kRecTile);
-    // Sequences of kOwnRows rows and more have chunks of their own; in shorter ones the last chunks, filled by half on the
-    // average, would cost more than the waiting that this saves.  That makes at most a 16th more chunks than the rows have.
-    const bool own = !offsets && nseq > 1 && T >= kOwnRows;
+    const bool own = nseq > 1 && own_chunks(nseq, T, tiles, elt);
     r->per_seq = own ? static_cast<int>(ceil_div(T, chunk_rows)) : 0;
     long long chunks = rows ? ceil_div(rows, chunk_rows) : 1;
     if (own) chunks = static_cast<long long>(r->per_seq) * nseq;
-    else if (nseq == 0) chunks += chunks / 16;
     if (chunks * tiles > kMaxBlocks) return abi_fail(CONV_ERR_UNSUPPORTED, "too many rows and channels for one launch");
     r->chunks = static_cast<int>(chunks);
     r->tiles = static_cast<int>(tiles);
@@ -311,28 +324,28 @@ int conv1d_causal_step(const void *x, const void *w, const void *bias, void *y, 
     return abi_ok();
 }
 
-int gated_recurrence_saved_size(long long rows, int C, conv_dtype_t dtype, size_t *bytes) {
+int gated_recurrence_saved_size(int nseq, int T, long long rows, int C, conv_dtype_t dtype, size_t *bytes) {
     RecLayout r;
     if (!bytes) return abi_fail(CONV_ERR_INVALID_ARG, "bytes must not be NULL");
-    RETURN_IF(rec_layout(nullptr, 0, 0, rows, C, dtype, true, &r));
-    // one for every kRecRun rows; up to a chunk behind the last row, and behind each sequence that has chunks of its own
-    const size_t states = static_cast<size_t>(ceil_div(rows, kRecRun)) + (rows / kOwnRows + 1) * (kRecSavedSpare + 1);
-    *bytes = states * r.Cpad * sizeof(float);
+    RETURN_IF(rec_layout(nseq, T, rows, C, dtype, true, &r));
+    // one for every kRecRun rows that have begun -- of each sequence, where each has chunks of its own
+    const size_t states = r.per_seq ? static_cast<size_t>(nseq) * ceil_div(T, kRecRun) : ceil_div(rows, kRecRun);
+    *bytes = std::max<size_t>(states, 1) * r.Cpad * sizeof(float);
     return abi_ok();
 }
 
-int gated_recurrence_workspace_size(long long rows, int C, conv_dtype_t dtype, size_t *bytes) {
+int gated_recurrence_workspace_size(int nseq, int T, long long rows, int C, conv_dtype_t dtype, size_t *bytes) {
     RecLayout r;
     if (!bytes) return abi_fail(CONV_ERR_INVALID_ARG, "bytes must not be NULL");
-    RETURN_IF(rec_layout(nullptr, 0, 0, rows, C, dtype, false, &r));
+    RETURN_IF(rec_layout(nseq, T, rows, C, dtype, false, &r));
     *bytes = r.forward_total;
     return abi_ok();
 }
 
-int gated_recurrence_backward_workspace_size(long long rows, int C, conv_dtype_t dtype, size_t *bytes) {
+int gated_recurrence_backward_workspace_size(int nseq, int T, long long rows, int C, conv_dtype_t dtype, size_t *bytes) {
     RecLayout r;
     if (!bytes) return abi_fail(CONV_ERR_INVALID_ARG, "bytes must not be NULL");
-    RETURN_IF(rec_layout(nullptr, 0, 0, rows, C, dtype, true, &r));
+    RETURN_IF(rec_layout(nseq, T, rows, C, dtype, true, &r));
     *bytes = r.backward_total;
     return abi_ok();
 }
@@ -353,7 +366,7 @@ int gated_recurrence_forward(const void *x, const void *gate_a, const void *gate
     RETURN_IF(check_state("state", state, "y", y, 4));
     RETURN_IF(check_state("saved", saved, "final_state", final_state, 16));
     RecLayout r;
-    RETURN_IF(rec_layout(offsets, nseq, T, rows, C, dtype, false, &r));
+    RETURN_IF(rec_layout(nseq, offsets ? 0 : T, rows, C, dtype, false, &r));
     RETURN_IF(check_workspace(workspace, workspace_bytes, r.forward_total));
     AbiDevice dev;
     RETURN_IF(abi_device(&dev));
@@ -391,7 +404,7 @@ int gated_recurrence_backward(const void *x, const void *gate_a, const void *gat
     RETURN_IF(check_state("saved", saved, "d_state", d_state, 16));
     RETURN_IF(check_state("d_decay", d_decay, "decay", decay, 4));
     RecLayout r;
-    RETURN_IF(rec_layout(offsets, nseq, T, rows, C, dtype, true, &r));
+    RETURN_IF(rec_layout(nseq, offsets ? 0 : T, rows, C, dtype, true, &r));
     RETURN_IF(check_workspace(workspace, workspace_bytes, r.backward_total));
     AbiDevice dev;
     RETURN_IF(abi_device(&dev));

@@ -27,9 +27,9 @@ SIGNATURES = {
     "conv1d_causal_backward_workspace_size": ([_L, _I, _I, ctypes.POINTER(_S)], _I),
     "conv1d_causal_backward": ([_P] * 10 + _SEQ + [_I, _I, _L, _L, _L, _I, _P, _S, _P], _I),
     "conv1d_causal_step": ([_P] * 6 + [_I] * 5 + [_L, _L, _I, _P], _I),
-    "gated_recurrence_saved_size": ([_L, _I, _I, ctypes.POINTER(_S)], _I),
-    "gated_recurrence_workspace_size": ([_L, _I, _I, ctypes.POINTER(_S)], _I),
-    "gated_recurrence_backward_workspace_size": ([_L, _I, _I, ctypes.POINTER(_S)], _I),
+    "gated_recurrence_saved_size": ([_I, _I, _L, _I, _I, ctypes.POINTER(_S)], _I),
+    "gated_recurrence_workspace_size": ([_I, _I, _L, _I, _I, ctypes.POINTER(_S)], _I),
+    "gated_recurrence_backward_workspace_size": ([_I, _I, _L, _I, _I, ctypes.POINTER(_S)], _I),
     "gated_recurrence_forward": ([_P] * 4 + [_F] + [_P] * 4 + _SEQ + [_L] * 4 + [_I, _P, _S, _P], _I),
     "gated_recurrence_backward": ([_P] * 4 + [_F] + [_P] * 9 + _SEQ + [_L] * 7 + [_I, _P, _S, _P], _I),
     "gated_recurrence_step": ([_P] * 4 + [_F] + [_P] * 3 + [_I] * 3 + [_L] * 4 + [_I, _P], _I),
@@ -48,18 +48,18 @@ def conv1d_causal_backward_workspace_size(rows, C, K) -> int:
 
 # These three depend on their arguments alone: asked once for each.
 @functools.lru_cache(maxsize=4096)
-def gated_recurrence_saved_size(rows, C, dtype) -> int:
-    return _size(load().gated_recurrence_saved_size, rows, C, dtype)
+def gated_recurrence_saved_size(nseq, T, rows, C, dtype) -> int:
+    return _size(load().gated_recurrence_saved_size, nseq, T, rows, C, dtype)
 
 
 @functools.lru_cache(maxsize=4096)
-def gated_recurrence_workspace_size(rows, C, dtype) -> int:
-    return _size(load().gated_recurrence_workspace_size, rows, C, dtype)
+def gated_recurrence_workspace_size(nseq, T, rows, C, dtype) -> int:
+    return _size(load().gated_recurrence_workspace_size, nseq, T, rows, C, dtype)
 
 
 @functools.lru_cache(maxsize=4096)
-def gated_recurrence_backward_workspace_size(rows, C, dtype) -> int:
-    return _size(load().gated_recurrence_backward_workspace_size, rows, C, dtype)
+def gated_recurrence_backward_workspace_size(nseq, T, rows, C, dtype) -> int:
+    return _size(load().gated_recurrence_backward_workspace_size, nseq, T, rows, C, dtype)
 
 
 # ------------------------------------------------------------ argument checks ---
@@ -284,16 +284,19 @@ class GatedRecurrenceB200:
             raise ValueError(f"x must be on {self.device}, not on {x.device}")
         return _dtype_code(x.dtype)
 
+    def _saved_floats(self, x, code):
+        packed = x.dim() == 2  # the size depends on the rows alone then, not on how they are cut
+        nseq, T, rows = (1, 0, x.shape[0]) if packed else (x.shape[0], x.shape[1], x.shape[0] * x.shape[1])
+        return gated_recurrence_saved_size(nseq, T, rows, self.C, code) // 4
+
     def saved_states(self, x):
         """A buffer for the states that the forward pass over x saves for its backward pass."""
         import torch
-        rows = x.numel() // max(1, x.shape[-1])
-        return torch.empty(gated_recurrence_saved_size(rows, self.C, _dtype_code(x.dtype)) // 4, dtype=torch.float32,
-                           device=x.device)
+        return torch.empty(self._saved_floats(x, _dtype_code(x.dtype)), dtype=torch.float32, device=x.device)
 
-    def _saved(self, saved, rows, code, device):
+    def _saved(self, saved, x, code):
         import torch
-        return _whole("saved", saved, (gated_recurrence_saved_size(rows, self.C, code) // 4,), torch.float32, device)
+        return _whole("saved", saved, (self._saved_floats(x, code),), torch.float32, x.device)
 
     def __call__(self, x, gate_a, gate_x, y=None, offsets=None, initial_state=None, final_state=None, saved=None,
                  stream=None):
@@ -306,12 +309,12 @@ class GatedRecurrenceB200:
         (px, ldx), (pa, lda), (pg, ldg) = _rows("x", x, x), _rows("gate_a", gate_a, x), _rows("gate_x", gate_x, x)
         state = _whole("initial_state", initial_state, (seq[1], self.C), torch.float32, x.device)
         final = _whole("final_state", final_state, (seq[1], self.C), torch.float32, x.device)
-        psaved = None if saved is None else self._saved(saved, seq[3], code, x.device)
+        psaved = None if saved is None else self._saved(saved, x, code)
 
         def call(s):
             out = _new(x) if y is None else y
             py, ldy = _rows("y", out, x)
-            ws = _scratch(gated_recurrence_workspace_size(seq[3], self.C, code), x.device)
+            ws = _scratch(gated_recurrence_workspace_size(*seq[1:], code), x.device)
             _check(load().gated_recurrence_forward(
                 px, pa, pg, self.decay.data_ptr(), self.kappa, py, state, final, psaved, *seq, ldx, lda, ldg, ldy, code,
                 None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), s))
@@ -330,14 +333,14 @@ class GatedRecurrenceB200:
         f32 = torch.float32
         state = _whole("initial_state", initial_state, (seq[1], self.C), f32, x.device)
         dfinal = _whole("d_final_state", d_final_state, (seq[1], self.C), f32, x.device)
-        psaved = self._saved(saved, seq[3], code, x.device)
+        psaved = self._saved(saved, x, code)
 
         def call(s):
             gx, ga, gg = (_new(x) if t is None else t for t in (dx, d_gate_a, d_gate_x))
             gd = _new(self.decay) if d_decay is None else d_decay
             gs = _new(initial_state) if d_initial_state is None and initial_state is not None else d_initial_state
             (pgx, ldgx), (pga, ldga), (pgg, ldgg) = _rows("dx", gx, x), _rows("d_gate_a", ga, x), _rows("d_gate_x", gg, x)
-            ws = _scratch(gated_recurrence_backward_workspace_size(seq[3], self.C, code), x.device)
+            ws = _scratch(gated_recurrence_backward_workspace_size(*seq[1:], code), x.device)
             _check(load().gated_recurrence_backward(
                 px, pa, pg, self.decay.data_ptr(), self.kappa, pdy, psaved, state, dfinal, pgx, pga, pgg,
                 _whole("d_decay", gd, (self.C,), f32, x.device),

@@ -84,12 +84,13 @@ int conv1d_causal_step(const void *x, const void *w, const void *bias, void *y, 
  * 0 * rx * x.  kappa: finite and above 0. */
 
 /* Bytes of the states that the forward pass saves for the backward pass (opaque): an fp32 state
- * for every 8 rows, an eighth of the bytes of y in fp32 and a quarter in bf16. */
-int gated_recurrence_saved_size(long long rows, int C, conv_dtype_t dtype, size_t *bytes);
+ * for every 8 rows, an eighth of the bytes of y in fp32 and a quarter in bf16.  T = 0: packed
+ * sequences (here and below). */
+int gated_recurrence_saved_size(int nseq, int T, long long rows, int C, conv_dtype_t dtype, size_t *bytes);
 
 /* Device scratch bytes of the forward pass, and of the backward pass. */
-int gated_recurrence_workspace_size(long long rows, int C, conv_dtype_t dtype, size_t *bytes);
-int gated_recurrence_backward_workspace_size(long long rows, int C, conv_dtype_t dtype, size_t *bytes);
+int gated_recurrence_workspace_size(int nseq, int T, long long rows, int C, conv_dtype_t dtype, size_t *bytes);
+int gated_recurrence_backward_workspace_size(int nseq, int T, long long rows, int C, conv_dtype_t dtype, size_t *bytes);
 
 /* The forward pass: y = h.
  *   state, final_state : (nseq, C) fp32, or NULL; final_state receives the last h of each
