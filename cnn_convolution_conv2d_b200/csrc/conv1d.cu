@@ -6,10 +6,12 @@
 // All three are bound by HBM: 2K + ~10 operations for 4 to 8 bytes.  A warp takes a strip of
 // rows of 32*V channels and slides down it with the last K-1 rows in registers, so each row
 // is read once (plus K-1 rows in front of a strip, which the neighbouring warp brings into L2).
-// Rows travel ahead of their use in a ring in shared memory, in which every thread copies and
-// reads its own places only: no barriers, and no registers or load counters held meanwhile (with
-// prefetched rows in registers a warp waited for its newest load at every row, 2.4 times slower,
-// or spilled).
+// Rows travel ahead of their use in a ring in shared memory that is the warp's own: no block
+// barriers, and no registers or load counters held meanwhile (with prefetched rows in registers a
+// warp waited for its newest load at every row, 2.4 times slower, or spilled).  Where TMA takes the
+// tensors, a lane loads a batch of rows with one instruction, the results take the places of the rows and
+// leave the same way: half the instructions of copies and stores by every thread, which is the form for
+// other strides and alignments.
 #include "ptx.cuh"
 #include "sequence.cuh"
 
@@ -49,21 +51,107 @@ __device__ __forceinline__ Raw<T, V> load_raw(const T *row, const Chan<T, V, kVe
 }
 
 // Copies a lane's channels of a row to its place in the ring, asynchronously where the copy
-// instruction has the size (4 bytes and more).
-template <typename T, int V, bool kVec>
-__device__ __forceinline__ void copy_ahead(Raw<T, V> *to, const T *row, const Chan<T, V, kVec> &ch) {
-    if constexpr (kVec) {
-        if (ch.any()) ptx::cp_async<sizeof(Raw<T, V>)>(to, row + ch.c);
-    } else if constexpr (sizeof(T) == 4) {
+// instruction has the size (4 bytes).
+template <typename T, int V>
+__device__ __forceinline__ void copy_ahead(Raw<T, V> *to, const T *row, const Chan<T, V, false> &ch) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (ch.has(v)) ptx::cp_async<4>(&to->v[v], row + ch.at(v));
+            if (ch.has(v)) ptx::cp_async_4(&to->v[v], row + ch.at(v));
     } else {
-        *to = load_raw<T, V, kVec>(row, ch);
+        *to = load_raw<T, V, false>(row, ch);
     }
 }
 
 constexpr int kRing = 3;  // batches in the ring: one at work, two on their way
+
+// A warp's ring of batches of U rows of N tensors.
+template <typename T, int V, int U, int N, bool kTma>
+struct Ring {
+    Raw<T, V> (*rows)[N][U][32];  // [kRing]
+    uint64_t *full;               // [kRing], TMA
+    int *abort;                   // the block's flag of waits that ran out
+    int slot = 0;
+    unsigned parity = 0;
+    int coming = 0;               // batches fetched and not waited for
+
+    // The batch of rows from `row` on, into the slot `ahead` places on; none from row1 on.
+    __device__ __forceinline__ void fetch(const CUtensorMap *maps, const T *const (&from)[N], const long long (&ld)[N], int row,
+                                          int row1, int tile, int ahead, const Chan<T, V, kTma> &ch) {
+        const int to = slot + ahead >= kRing ? slot + ahead - kRing : slot + ahead;
+        if (row < row1) ++coming;
+        if constexpr (kTma) {
+            __syncwarp();
+            if (row < row1 && (threadIdx.x & 31) == 0) {
+                ptx::bulk_wait_group_read<0>();  // what left from this slot
+                ptx::fence_proxy_async_smem();
+                ptx::mbar_arrive_expect_tx(&full[to], N * U * 32 * sizeof(Raw<T, V>));
+#pragma unroll
+                for (int i = 0; i < N; ++i) ptx::tma_load_2d(&rows[to][i][0][0], maps + i, &full[to], tile * 32 * V, row);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (row + u < row1) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        copy_ahead<T, V>(&rows[to][i][u][threadIdx.x & 31], from[i] + static_cast<size_t>(row + u) * ld[i], ch);
+                }
+            ptx::cp_async_commit();
+        }
+    }
+    __device__ __forceinline__ bool wait(const Conv1dParams &p) {
+        if constexpr (kTma) {
+            const ptx::Watchdog wd{abort, p.status, static_cast<uint64_t>(p.timeout_ns)};
+            if (!ptx::mbar_wait(&full[slot], parity, wd, kDevTimeoutFull)) return false;
+        } else {
+            ptx::cp_async_wait<1>();
+        }
+        --coming;
+        return true;
+    }
+    // Nothing may be on its way into or out of the ring when its block ends.
+    __device__ __forceinline__ void drain(const Conv1dParams &p) {
+        if constexpr (kTma) {
+            for (; coming > 0; next()) {  // a wait ran out: once more, and for the others, within the limit
+                *abort = 0;
+                if (!wait(p)) --coming;
+            }
+            if ((threadIdx.x & 31) == 0) ptx::bulk_wait_group_read<0>();
+        }
+    }
+    __device__ __forceinline__ Raw<T, V> &at(int i, int u) { return rows[slot][i][u][threadIdx.x & 31]; }
+    __device__ __forceinline__ void next() {
+        if (++slot == kRing) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
+    // Sends the batch's first tensor, whose rows are results now, to the rows from `row` on.
+    __device__ __forceinline__ void send(const CUtensorMap *map, int tile, int row) {
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+            ptx::tma_store_2d(map, &rows[slot][0][0][0], tile * 32 * V, row);
+            ptx::bulk_commit_group();
+        }
+    }
+};
+
+// The block's rings in shared memory.
+template <typename T, int V, int U, int N, bool kTma>
+__device__ __forceinline__ Ring<T, V, U, N, kTma> make_ring(Raw<T, V> (*s_rows)[kRing][N][U][32]) {
+    __shared__ uint64_t s_full[kConvWarps][kRing];
+    __shared__ int s_abort;
+    const int warp = threadIdx.x >> 5;
+    if constexpr (kTma) {
+        if (threadIdx.x % 32 == 0) s_abort = 0;  // (every warp the same)
+        if ((threadIdx.x & 31) < kRing) ptx::mbar_init(&s_full[warp][threadIdx.x & 31], 1);
+        ptx::fence_mbar_init();
+        __syncwarp();
+    }
+    return Ring<T, V, U, N, kTma>{s_rows[warp], s_full[warp], &s_abort};
+}
 
 // V channels as pairs: the arithmetic runs two channels to an instruction.
 template <int V> struct Pairs { float2 p[V / 2]; };
@@ -94,6 +182,7 @@ __device__ __forceinline__ void add_product(Pairs<V> &sum, const Pairs<V> &a, co
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) sum.p[i] = __ffma2_rn(a.p[i], b.p[i], sum.p[i]);
 }
+// 1 / (1 + e^-z).  Where e^-z passes the largest float, 1/inf = 0 is the right value.
 template <int V>
 __device__ __forceinline__ Pairs<V> sigmoid(const Pairs<V> &z) {
     Pairs<V> r;
@@ -131,8 +220,8 @@ __device__ __forceinline__ Pairs<V> load(const T *row, const Chan<T, V, kVec> &c
     return pairs<T, V>(load_raw<T, V, kVec>(row, ch));
 }
 
-template <typename T, int V, bool kVec>
-__device__ __forceinline__ void store(T *row, const Pairs<V> &f, const Chan<T, V, kVec> &ch) {
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> pack(const Pairs<V> &f) {
     Raw<T, V> r;
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
@@ -143,6 +232,12 @@ __device__ __forceinline__ void store(T *row, const Pairs<V> &f, const Chan<T, V
             r.v[2 * i + 1] = f.p[i].y;
         }
     }
+    return r;
+}
+
+template <typename T, int V, bool kVec>
+__device__ __forceinline__ void store(T *row, const Pairs<V> &f, const Chan<T, V, kVec> &ch) {
+    Raw<T, V> r = pack<T, V>(f);
     if constexpr (kVec) {
         if (ch.any()) {
             if constexpr (sizeof(r) == 16) *reinterpret_cast<uint4 *>(row + ch.c) = *reinterpret_cast<uint4 *>(&r);
@@ -249,8 +344,9 @@ __device__ __forceinline__ void shift_in(Pairs<V> (&win)[N], const Pairs<V> &row
 }
 
 template <typename T, int K, int V, bool kVec>
-__global__ void __launch_bounds__(kConvWarps * 32, 6) conv1d_forward_kernel(const __grid_constant__ Conv1dParams p) {
-    constexpr int U = 8 * 2 / sizeof(T);
+__global__ void __launch_bounds__(kConvWarps * 32, kConvBlocks) conv1d_forward_kernel(const __grid_constant__ Conv1dTiles q) {
+    constexpr int U = kConvBatch / sizeof(T);
+    const Conv1dParams &p = q.p;
     const int tile = blockIdx.x % p.tiles, block = blockIdx.x / p.tiles;  // neighbours share rows
     const Chan<T, V, kVec> ch(tile, p.C);
     if (blockIdx.x == 0) check_offsets(p.seq, p.status);
@@ -261,17 +357,13 @@ __global__ void __launch_bounds__(kConvWarps * 32, 6) conv1d_forward_kernel(cons
     const long long first = (static_cast<long long>(block) * kConvWarps + (threadIdx.x >> 5)) * p.strip;
     if (first >= p.seq.rows) return;
     const int row0 = static_cast<int>(first), row1 = min(p.seq.rows - row0, p.strip) + row0;
-    const T *x = static_cast<const T *>(p.x) + static_cast<size_t>(row0) * p.ldx;
-    T *y = static_cast<T *>(p.y) + static_cast<size_t>(row0) * p.ldy;
-    __shared__ Raw<T, V> s_ring[kRing][U][kConvWarps * 32];
-    auto fetch = [&](int row, const T *from, int slot) {  // the batch of rows from `row` on
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (row + u < row1) copy_ahead<T, V, kVec>(&s_ring[slot][u][threadIdx.x], from + u * p.ldx, ch);
-        ptx::cp_async_commit();
-    };
-    fetch(row0, x, 0);
-    fetch(row0 + U, x + U * p.ldx, 1);
+    const T *x = static_cast<const T *>(p.x);
+    T *y = static_cast<T *>(p.y);
+    __shared__ __align__(128) Raw<T, V> s_rows[kConvWarps][kRing][1][U][32];
+    auto ring = make_ring<T, V, U, 1, kVec>(s_rows);
+    auto fetch = [&](int row, int ahead) { ring.fetch(&q.in[0], {x}, {p.ldx}, row, row1, tile, ahead, ch); };
+    fetch(row0, 0);
+    fetch(row0 + U, 1);
     Pairs<V> w[K], b, win[K - 1];
     load_weights<T, K, V, kVec>(w, b, p.w, p.bias, ch);
     Cursor cur;
@@ -283,22 +375,25 @@ __global__ void __launch_bounds__(kConvWarps * 32, 6) conv1d_forward_kernel(cons
         for (int k = 0; k < K; ++k) add_product<V>(z, w[k], rows[k]);
         return p.silu ? mul<V>(z, sigmoid<V>(z)) : z;
     };
-    int slot = 0;
-    for (int row = row0; row < row1; row += U) {
-        fetch(row + 2 * U, x + 2 * U * p.ldx, slot ? slot - 1 : kRing - 1);
-        ptx::cp_async_wait<kRing - 1>();
+    for (int row = row0; row < row1; row += U, ring.next()) {
+        if (!ring.wait(p)) break;
         if (cur.inside(p.seq) && row + U <= min(cur.end, row1)) {
             Pairs<V> all[K - 1 + U];
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) all[j] = win[j];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                all[K - 1 + u] = pairs<T, V>(s_ring[slot][u][threadIdx.x]);
-                store<T, V, kVec>(y + u * p.ldy, result(all + u), ch);
+                if (u == U / 2) fetch(row + 2 * U, 2);  // by now what the last batch left has gone
+                Raw<T, V> &at = ring.at(0, u);
+                all[K - 1 + u] = pairs<T, V>(at);
+                if constexpr (kVec) at = pack<T, V>(result(all + u));
+                else store<T, V, kVec>(y + static_cast<size_t>(row + u) * p.ldy, result(all + u), ch);
             }
+            if constexpr (kVec) ring.send(&q.out, tile, row);
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) win[j] = all[U + j];
         } else {  // a sequence or the strip ends here: row by row
+            fetch(row + 2 * U, 2);
 #pragma unroll 1
             for (int u = 0; u < U && row + u < row1; ++u) {
                 if (row + u >= cur.end) {
@@ -308,15 +403,13 @@ __global__ void __launch_bounds__(kConvWarps * 32, 6) conv1d_forward_kernel(cons
                 Pairs<V> all[K];
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j) all[j] = win[j];
-                all[K - 1] = pairs<T, V>(s_ring[slot][u][threadIdx.x]);
-                if (cur.inside(p.seq)) store<T, V, kVec>(y + u * p.ldy, result(all), ch);
+                all[K - 1] = pairs<T, V>(ring.at(0, u));
+                if (cur.inside(p.seq)) store<T, V, kVec>(y + static_cast<size_t>(row + u) * p.ldy, result(all), ch);
                 shift_in<K - 1, V>(win, all[K - 1]);
             }
         }
-        slot = slot == kRing - 1 ? 0 : slot + 1;
-        x += U * p.ldx;
-        y += U * p.ldy;
     }
+    ring.drain(p);
 }
 
 // Backward.  Going down the rows, row t's dz completes the gradient of row t-(K-1):
@@ -324,10 +417,9 @@ __global__ void __launch_bounds__(kConvWarps * 32, 6) conv1d_forward_kernel(cons
 // sequence; a target ahead of the sequence is a row of the carried window).  K-1 rows behind the strip
 // are read for the dz's that its last rows still need.
 template <typename T, int K, int V, bool kVec>
-__global__ void __launch_bounds__(kConvWarps * 32, 4) conv1d_backward_kernel(const __grid_constant__ Conv1dParams p) {
-    constexpr int U = 4 * 2 / sizeof(T);
-    __shared__ float2 s_sum[kConvWarps][16 * V];
-    __shared__ Raw<T, V> s_ring[kRing][2][U][kConvWarps * 32];
+__global__ void __launch_bounds__(kConvWarps * 32, kConvBlocksBack) conv1d_backward_kernel(const __grid_constant__ Conv1dTiles q) {
+    constexpr int U = kConvBatch / sizeof(T);
+    const Conv1dParams &p = q.p;
     const int tile = blockIdx.x % p.tiles, block = blockIdx.x / p.tiles;  // neighbours share rows
     const Chan<T, V, kVec> ch(tile, p.C);
     if (blockIdx.x == 0) check_offsets(p.seq, p.status);
@@ -340,6 +432,10 @@ __global__ void __launch_bounds__(kConvWarps * 32, 4) conv1d_backward_kernel(con
                               load_state<T, K, V, kVec>(p.d_final, s, K - 1 - j, ch), ch);
         return;
     }
+    extern __shared__ __align__(128) uint8_t s_dynamic[];
+    auto s_rows = reinterpret_cast<Raw<T, V> (*)[kRing][2][U][32]>(s_dynamic);
+    float2 (*s_sum)[16 * V] = reinterpret_cast<float2 (*)[16 * V]>(s_dynamic);  // once the rings are done with
+    auto ring = make_ring<T, V, U, 2, kVec>(s_rows);
     Pairs<V> w[K], b, dw[K], db = zero_pairs<V>();
 #pragma unroll
     for (int k = 0; k < K; ++k) dw[k] = zero_pairs<V>();
@@ -347,20 +443,11 @@ __global__ void __launch_bounds__(kConvWarps * 32, 4) conv1d_backward_kernel(con
     if (first < p.seq.rows) {
         const int row0 = static_cast<int>(first), row1 = min(p.seq.rows - row0, p.strip) + row0;
         const int last = min(p.seq.rows - row1, K - 1) + row1;  // rows read
-        const T *x = static_cast<const T *>(p.x) + static_cast<size_t>(row0) * p.ldx;
-        const T *dy = static_cast<const T *>(p.dy) + static_cast<size_t>(row0) * p.lddy;
+        const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy);
         T *dx = static_cast<T *>(p.y);
-        auto fetch = [&](int row, const T *from_x, const T *from_d, int slot) {  // the batch of rows from `row` on
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (row + u < last) {
-                    copy_ahead<T, V, kVec>(&s_ring[slot][0][u][threadIdx.x], from_x + u * p.ldx, ch);
-                    copy_ahead<T, V, kVec>(&s_ring[slot][1][u][threadIdx.x], from_d + u * p.lddy, ch);
-                }
-            ptx::cp_async_commit();
-        };
-        fetch(row0, x, dy, 0);
-        fetch(row0 + U, x + U * p.ldx, dy + U * p.lddy, 1);
+        auto fetch = [&](int row, int ahead) { ring.fetch(&q.in[0], {x, dy}, {p.ldx, p.lddy}, row, last, tile, ahead, ch); };
+        fetch(row0, 0);
+        fetch(row0 + U, 1);
         load_weights<T, K, V, kVec>(w, b, p.w, p.bias, ch);
         Pairs<V> win[K - 1], past[K - 1];  // x and dz of the K-1 rows before
         Cursor cur;
@@ -410,13 +497,13 @@ __global__ void __launch_bounds__(kConvWarps * 32, 4) conv1d_backward_kernel(con
             }
         };
         bool done = false;
-        int slot = 0;
-        for (int row = row0; row < last && !done; row += U) {
-            fetch(row + 2 * U, x + 2 * U * p.ldx, dy + 2 * U * p.lddy, slot ? slot - 1 : kRing - 1);
-            ptx::cp_async_wait<kRing - 1>();
+        for (int row = row0; row < last; row += U, ring.next()) {
+            if (!ring.wait(p)) break;
+            if (done) continue;  // (two batches at most: K-1 rows behind the strip)
             if (cur.inside(p.seq) && row + U <= cur.end && row - (K - 1) >= cur.begin) {
                 Pairs<V> all[K - 1 + U], dz[K - 1 + U];
-                T *to = dx + static_cast<ptrdiff_t>(row - (K - 1)) * p.ldy;
+                const int target = row - (K - 1);  // the first of the rows whose gradients are finished
+                const bool bulk = kVec && target >= row0 && target + U <= row1;
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j) {
                     all[j] = win[j];
@@ -425,18 +512,24 @@ __global__ void __launch_bounds__(kConvWarps * 32, 4) conv1d_backward_kernel(con
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int t = row + u;
-                    all[K - 1 + u] = pairs<T, V>(s_ring[slot][0][u][threadIdx.x]);
-                    dz[K - 1 + u] = slope(pairs<T, V>(s_ring[slot][1][u][threadIdx.x]), all + u);
+                    if (u == U / 2) fetch(row + 2 * U, 2);
+                    Raw<T, V> &at = ring.at(0, u);
+                    all[K - 1 + u] = pairs<T, V>(at);
+                    dz[K - 1 + u] = slope(pairs<T, V>(ring.at(1, u)), all + u);
                     if (t < row1) sums(dz[K - 1 + u], all + u);
-                    if (t - (K - 1) >= row0 && t - (K - 1) < row1)  // (rows behind `last` hold nothing, and end here)
-                        store<T, V, kVec>(to + u * p.ldy, gradient(dz + u), ch);
+                    const Pairs<V> g = gradient(dz + u);
+                    if (bulk) at = pack<T, V>(g);
+                    else if (target + u >= row0 && target + u < row1)  // (rows behind `last` hold nothing, and end here)
+                        store<T, V, kVec>(dx + static_cast<size_t>(target + u) * p.ldy, g, ch);
                 }
+                if (bulk) ring.send(&q.out, tile, target);
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j) {
                     win[j] = all[U + j];
                     past[j] = dz[U + j];
                 }
             } else {  // a sequence begins or ends here: row by row
+                fetch(row + 2 * U, 2);
 #pragma unroll 1
                 for (int u = 0; u < U && row + u < last; ++u) {
                     const int t = row + u;
@@ -460,20 +553,18 @@ __global__ void __launch_bounds__(kConvWarps * 32, 4) conv1d_backward_kernel(con
                         all[j] = win[j];
                         dz[j] = past[j];
                     }
-                    all[K - 1] = pairs<T, V>(s_ring[slot][0][u][threadIdx.x]);
-                    dz[K - 1] = slope(pairs<T, V>(s_ring[slot][1][u][threadIdx.x]), all);
+                    all[K - 1] = pairs<T, V>(ring.at(0, u));
+                    dz[K - 1] = slope(pairs<T, V>(ring.at(1, u)), all);
                     if (t < row1) sums(dz[K - 1], all);
                     emit(t, gradient(dz));
                     shift_in<K - 1, V>(win, all[K - 1]);
                     shift_in<K - 1, V>(past, dz[K - 1]);
                 }
             }
-            slot = slot == kRing - 1 ? 0 : slot + 1;
-            x += U * p.ldx;
-            dy += U * p.lddy;
         }
         // the rows ended with this sequence
         if (!done && cur.inside(p.seq) && last >= cur.end) flush();
+        ring.drain(p);
     }
     // The block's sums of dw and db: its warps' in order, so that equal inputs give equal bits.
 #pragma unroll
@@ -548,18 +639,24 @@ __global__ void __launch_bounds__(128) conv1d_step_kernel(const __grid_constant_
 constexpr int lane_channels(int K) { return K <= 4 ? 4 : 2; }
 
 template <typename T, bool kVec, int K>
-cudaError_t forward_k(const Conv1dParams &p, cudaStream_t s) {
+cudaError_t forward_k(const Conv1dTiles &q, cudaStream_t s) {
     constexpr int V = lane_channels(K);
+    const Conv1dParams &p = q.p;
     const int grid = p.tiles * (p.row_blocks + (p.final_state ? p.seq.nseq : 0));
-    conv1d_forward_kernel<T, K, V, kVec><<<grid, kConvWarps * 32, 0, s>>>(p);
+    conv1d_forward_kernel<T, K, V, kVec><<<grid, kConvWarps * 32, 0, s>>>(q);
     return cudaGetLastError();
 }
 
 template <typename T, bool kVec, int K>
-cudaError_t backward_k(const Conv1dParams &p, cudaStream_t s) {
+cudaError_t backward_k(const Conv1dTiles &q, cudaStream_t s) {
     constexpr int V = lane_channels(K);
+    const Conv1dParams &p = q.p;
     const int grid = p.tiles * (p.row_blocks + (p.d_state ? p.seq.nseq : 0));
-    conv1d_backward_kernel<T, K, V, kVec><<<grid, kConvWarps * 32, 0, s>>>(p);
+    constexpr size_t smem = kConvWarps * kRing * 2 * (kConvBatch / sizeof(T)) * 32 * sizeof(Raw<T, V>);
+    const auto kernel = conv1d_backward_kernel<T, K, V, kVec>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kConvWarps * 32, smem, s>>>(q);
     return cudaGetLastError();
 }
 
@@ -570,8 +667,8 @@ cudaError_t step_k(const Conv1dStepParams &p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-#define CONV1D_BY_K(fn, p, s)                   \
-    switch ((p).K) {                            \
+#define CONV1D_BY_K(fn, k, p, s)                \
+    switch (k) {                                \
         case 2: return fn<T, kVec, 2>(p, s);    \
         case 3: return fn<T, kVec, 3>(p, s);    \
         case 4: return fn<T, kVec, 4>(p, s);    \
@@ -582,30 +679,41 @@ cudaError_t step_k(const Conv1dStepParams &p, cudaStream_t s) {
         default: return cudaErrorInvalidValue;  \
     }
 
-template <typename T, bool kVec> cudaError_t forward_t(const Conv1dParams &p, cudaStream_t s) { CONV1D_BY_K(forward_k, p, s) }
-template <typename T, bool kVec> cudaError_t backward_t(const Conv1dParams &p, cudaStream_t s) { CONV1D_BY_K(backward_k, p, s) }
-template <typename T, bool kVec> cudaError_t step_t(const Conv1dStepParams &p, cudaStream_t s) { CONV1D_BY_K(step_k, p, s) }
+template <typename T, bool kVec> cudaError_t forward_t(const Conv1dTiles &q, cudaStream_t s) { CONV1D_BY_K(forward_k, q.p.K, q, s) }
+template <typename T, bool kVec> cudaError_t backward_t(const Conv1dTiles &q, cudaStream_t s) { CONV1D_BY_K(backward_k, q.p.K, q, s) }
+template <typename T, bool kVec> cudaError_t step_t(const Conv1dStepParams &p, cudaStream_t s) { CONV1D_BY_K(step_k, p.K, p, s) }
 
 }  // namespace
 
 int conv1d_channels_per_block(int K) { return 32 * lane_channels(K); }
 
-// Rows of a warp's strip: 64, fewer where that leaves SMs without a block.
-int conv1d_strip(int rows, int C, int K, int sms) {
+// Rows of a warp's strip, a multiple of 8.  Forward: 64, fewer where that leaves SMs without a block.  Backward, which
+// has fewer warps on an SM: up to 128, so that the rounds of blocks on the device, each as long as a strip and what it
+// costs to begin one (some 12 rows' time), take the least together.  At 16384 rows of 4096 channels the last round of
+// strips of 64 is mostly empty: backward 115 -> 105 us, while forward, whose warps wait for memory, loses (55 -> 57 us).
+int conv1d_strip(int rows, int C, int K, int sms, bool back) {
     const long long tiles = (C + conv1d_channels_per_block(K) - 1) / conv1d_channels_per_block(K);
-    int strip = 64;
-    while (strip > 8 && tiles * ((rows + kConvWarps * strip - 1) / (kConvWarps * strip)) < 4LL * sms) strip >>= 1;
-    return strip;
+    const auto blocks = [&](int strip) { return tiles * ((rows + kConvWarps * strip - 1LL) / (kConvWarps * strip)); };
+    int best = 64;
+    if (!back || sms < 1) {
+        while (best > 8 && blocks(best) < 4LL * sms) best >>= 1;
+        return best;
+    }
+    const long long resident = static_cast<long long>(sms) * kConvBlocksBack;
+    const auto time = [&](int strip) { return (blocks(strip) + resident - 1) / resident * (strip + 12); };
+    for (int strip = 8; strip <= 128; strip += 8)
+        if (time(strip) < time(best) || (time(strip) == time(best) && strip > best)) best = strip;
+    return best;
 }
 
-cudaError_t launch_conv1d_forward(const Conv1dParams &p, bool f32, bool vec, cudaStream_t s) {
-    if (f32) return vec ? forward_t<float, true>(p, s) : forward_t<float, false>(p, s);
-    return vec ? forward_t<__nv_bfloat16, true>(p, s) : forward_t<__nv_bfloat16, false>(p, s);
+cudaError_t launch_conv1d_forward(const Conv1dTiles &q, bool f32, bool tma, cudaStream_t s) {
+    if (f32) return tma ? forward_t<float, true>(q, s) : forward_t<float, false>(q, s);
+    return tma ? forward_t<__nv_bfloat16, true>(q, s) : forward_t<__nv_bfloat16, false>(q, s);
 }
 
-cudaError_t launch_conv1d_backward(const Conv1dParams &p, bool f32, bool vec, cudaStream_t s) {
-    if (f32) return vec ? backward_t<float, true>(p, s) : backward_t<float, false>(p, s);
-    return vec ? backward_t<__nv_bfloat16, true>(p, s) : backward_t<__nv_bfloat16, false>(p, s);
+cudaError_t launch_conv1d_backward(const Conv1dTiles &q, bool f32, bool tma, cudaStream_t s) {
+    if (f32) return tma ? backward_t<float, true>(q, s) : backward_t<float, false>(q, s);
+    return tma ? backward_t<__nv_bfloat16, true>(q, s) : backward_t<__nv_bfloat16, false>(q, s);
 }
 
 cudaError_t launch_conv1d_reduce(const float *partial, void *dw, void *db, int row_blocks, int C, int K, bool f32,

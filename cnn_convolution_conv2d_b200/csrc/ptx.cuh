@@ -129,13 +129,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const 
 }
 
 // ----------------------------------------------- asynchronous copies by threads ---
-// Copies kBytes (4, 8 or 16, aligned to that) to shared memory; a thread waits for its own copies.
-template <int kBytes>
-__device__ __forceinline__ void cp_async(void *to, const void *from) {
-    if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(to)), "l"(from), "n"(kBytes) : "memory");
+// Copies 4 bytes, aligned to that, to shared memory; a thread waits for its own copies.
+__device__ __forceinline__ void cp_async_4(void *to, const void *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(to)), "l"(from) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most kPending of the thread's committed groups are outstanding.

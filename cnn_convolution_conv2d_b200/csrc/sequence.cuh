@@ -36,6 +36,14 @@ struct Conv1dParams {
     int tiles;             // channel tiles
     int row_blocks;        // blocks of kConvWarps strips; blocks behind them copy states
     int *status;
+    long long timeout_ns;
+};
+
+// The convolution with rows that travel by TMA, in boxes of a warp's channels x kConvBatch / sizeof(element) rows.
+struct Conv1dTiles {
+    CUtensorMap in[2];     // x, dy
+    CUtensorMap out;       // y or dx
+    Conv1dParams p;
 };
 
 struct Conv1dStepParams {
@@ -93,6 +101,8 @@ struct RecStepParams {
 };
 
 constexpr int kConvWarps = 4;     // warps of a conv1d block, one strip of rows each
+constexpr int kConvBlocks = 6, kConvBlocksBack = 4;  // blocks an SM
+constexpr int kConvBatch = 16;    // bytes of one channel's rows in a batch: 8 rows in bf16, 4 in fp32
 constexpr int kRecTile = 64;      // channels of a work item of the recurrence
 constexpr int kRecRun = 8;        // rows of one saved state
 
@@ -105,12 +115,12 @@ constexpr RecShape rec_shape(int elt, bool back) {
     return back ? (elt == 2 ? RecShape{7, 8, 2, 2} : RecShape{6, 8, 2, 2}) : (elt == 2 ? RecShape{8, 16, 2, 2} : RecShape{8, 8, 2, 2});
 }
 
-cudaError_t launch_conv1d_forward(const Conv1dParams &p, bool f32, bool vec, cudaStream_t s);
-cudaError_t launch_conv1d_backward(const Conv1dParams &p, bool f32, bool vec, cudaStream_t s);
+cudaError_t launch_conv1d_forward(const Conv1dTiles &q, bool f32, bool tma, cudaStream_t s);
+cudaError_t launch_conv1d_backward(const Conv1dTiles &q, bool f32, bool tma, cudaStream_t s);
 cudaError_t launch_conv1d_reduce(const float *partial, void *dw, void *db, int row_blocks, int C, int K, bool f32,
                                  cudaStream_t s);
 cudaError_t launch_conv1d_step(const Conv1dStepParams &p, bool f32, bool vec, cudaStream_t s);
-int conv1d_strip(int rows, int C, int K, int sms);
+int conv1d_strip(int rows, int C, int K, int sms, bool back);
 int conv1d_channels_per_block(int K);
 
 cudaError_t launch_rec_init(const RecParams &p, size_t words, float *rates, cudaStream_t s);
@@ -190,9 +200,6 @@ __device__ __forceinline__ float sqrt_approx(float x) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
-
-// 1 / (1 + e^-z).  Where e^-z passes the largest float, 1/inf = 0 is the right value.
-__device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.f + ex2_approx(z * -kLog2e)); }
 
 #endif  // __CUDACC__
 

@@ -92,9 +92,16 @@ int sms_or_zero() {
 }
 
 // Blocks of kConvWarps strips over the rows, and the strip.
-long long conv_row_blocks(long long rows, int C, int K, int sms, int *strip) {
-    *strip = conv1d_strip(static_cast<int>(rows), C, K, sms);
+long long conv_row_blocks(long long rows, int C, int K, int sms, bool back, int *strip) {
+    *strip = conv1d_strip(static_cast<int>(rows), C, K, sms, back);
     return ceil_div(rows, static_cast<long long>(*strip) * kConvWarps);
+}
+
+// A tensor over rows as a tensor map of {C, rows}; false where TMA does not take it.
+bool tile_map(const void *ptr, long long stride, long long rows, int C, int elt, int box_cols, int box_rows, CUtensorMap *map) {
+    const long long bytes = stride * elt;
+    if (rows < 1 || stride < C || bytes % 16 || bytes >= 1LL << 40 || !aligned(ptr, 16)) return false;
+    return abi_tensor_map_2d(map, ptr, elt, C, rows, bytes, box_cols, box_rows) == CONV_OK;
 }
 
 // The recurrence's scratch: [counter][aggregates][carries][decay rates][decay sums], each at a multiple of 256 bytes.
@@ -163,26 +170,19 @@ int rec_begin(RecParams *p, const RecLayout &r, void *workspace, cudaStream_t st
     return abi_launch(launch_rec_init(*p, r.rates / 4, rates, stream), "recurrence scratch");
 }
 
-// A tensor over rows as a tensor map of {C, rows}, boxes of kRecTile x box_rows; false where TMA does not take it.
-bool tile_map(const void *ptr, long long stride, long long rows, int C, int elt, int box_rows, CUtensorMap *map) {
-    const long long bytes = stride * elt;
-    if (rows < 1 || stride < C || bytes % 16 || bytes >= 1LL << 40 || !aligned(ptr, 16)) return false;
-    return abi_tensor_map_2d(map, ptr, elt, C, rows, bytes, kRecTile, box_rows) == CONV_OK;
-}
-
 // Runs the recurrence: in tiles where TMA takes every tensor, element by element otherwise.
 int run_rec(const RecParams &p, const RecLayout &r, int elt, bool back, cudaStream_t s) {
     RecTiles q{};
     const long long rows = p.seq.rows;
     const int run = rec_shape(elt, back).run, chunk = r.chunk_rows;
-    bool tiles = tile_map(p.x, p.ldx, rows, p.C, elt, chunk, &q.in[0]) &&
-                 tile_map(p.ga, p.lda, rows, p.C, elt, chunk, &q.in[1]) &&
-                 tile_map(p.gx, p.ldg, rows, p.C, elt, chunk, &q.in[2]) &&
-                 tile_map(p.y, p.ldy, rows, p.C, elt, run, &q.out[0]);
+    bool tiles = tile_map(p.x, p.ldx, rows, p.C, elt, kRecTile, chunk, &q.in[0]) &&
+                 tile_map(p.ga, p.lda, rows, p.C, elt, kRecTile, chunk, &q.in[1]) &&
+                 tile_map(p.gx, p.ldg, rows, p.C, elt, kRecTile, chunk, &q.in[2]) &&
+                 tile_map(p.y, p.ldy, rows, p.C, elt, kRecTile, run, &q.out[0]);
     if (back)
-        tiles = tiles && tile_map(p.dy, p.lddy, rows, p.C, elt, chunk, &q.in[3]) &&
-                tile_map(p.dga, p.ld_da, rows, p.C, elt, run, &q.out[1]) &&
-                tile_map(p.dgx, p.ld_dg, rows, p.C, elt, run, &q.out[2]);
+        tiles = tiles && tile_map(p.dy, p.lddy, rows, p.C, elt, kRecTile, chunk, &q.in[3]) &&
+                tile_map(p.dga, p.ld_da, rows, p.C, elt, kRecTile, run, &q.out[1]) &&
+                tile_map(p.dgx, p.ld_dg, rows, p.C, elt, kRecTile, run, &q.out[2]);
     const char *what = back ? "recurrence gradient" : "recurrence";
     if (!tiles) return abi_launch(launch_rec_plain(p, elt == 4, back, s), what);
     q.p = p;
@@ -227,18 +227,23 @@ int conv1d_causal_forward(const void *x, const void *w, const void *bias, void *
     wide = wide && wide_state(state, lanes * elt) && wide_state(final_state, lanes * elt);
     AbiDevice dev;
     RETURN_IF(abi_device(&dev));
-    Conv1dParams p{};
+    Conv1dTiles q{};
+    Conv1dParams &p = q.p;
+    p.timeout_ns = dev.timeout_ns;
     p.x = x; p.w = w; p.bias = bias; p.y = y; p.state = state; p.final_state = final_state;
     p.ldx = x_stride; p.ldy = y_stride;
     p.seq = Sequences{offsets, nseq, T, static_cast<int>(rows)};
     p.C = C; p.K = K; p.silu = activation == CONV_ACT_SILU; p.status = dev.status;
     p.tiles = static_cast<int>(ceil_div(C, conv1d_channels_per_block(K)));
-    const long long blocks = conv_row_blocks(rows, C, K, dev.sms, &p.strip);
+    const long long blocks = conv_row_blocks(rows, C, K, dev.sms, false, &p.strip);
     const long long all = (blocks + (final_state ? nseq : 0)) * p.tiles;
     if (all > kMaxBlocks) return abi_fail(CONV_ERR_UNSUPPORTED, "too many rows and channels for one launch");
     p.row_blocks = static_cast<int>(blocks);
+    const int box = conv1d_channels_per_block(K), batch = kConvBatch / elt;
+    const bool tma = wide && tile_map(x, x_stride, rows, C, elt, box, batch, &q.in[0]) &&
+                     tile_map(y, y_stride, rows, C, elt, box, batch, &q.out);
     if (all > 0)
-        RETURN_IF(abi_launch(launch_conv1d_forward(p, elt == 4, wide, reinterpret_cast<cudaStream_t>(stream)),
+        RETURN_IF(abi_launch(launch_conv1d_forward(q, elt == 4, tma, reinterpret_cast<cudaStream_t>(stream)),
                              "causal convolution"));
     return abi_ok();
 }
@@ -248,7 +253,7 @@ int conv1d_causal_backward_workspace_size(long long rows, int C, int K, size_t *
     RETURN_IF(check_conv(K, CONV_ACT_NONE));
     if (rows > kMaxRows) return abi_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows");
     int strip = 0;
-    *bytes = static_cast<size_t>(conv_row_blocks(rows, C, K, sms_or_zero(), &strip)) * (K + 1) * C * sizeof(float);
+    *bytes = static_cast<size_t>(conv_row_blocks(rows, C, K, sms_or_zero(), true, &strip)) * (K + 1) * C * sizeof(float);
     return abi_ok();
 }
 
@@ -274,21 +279,27 @@ int conv1d_causal_backward(const void *x, const void *w, const void *bias, const
            wide_state(d_state, lanes * elt);
     AbiDevice dev;
     RETURN_IF(abi_device(&dev));
-    Conv1dParams p{};
+    Conv1dTiles q{};
+    Conv1dParams &p = q.p;
+    p.timeout_ns = dev.timeout_ns;
     p.x = x; p.w = w; p.bias = bias; p.dy = dy; p.y = dx; p.state = state; p.d_final = d_final_state;
     p.d_state = d_state;
     p.ldx = x_stride; p.ldy = dx_stride; p.lddy = dy_stride;
     p.seq = Sequences{offsets, nseq, T, static_cast<int>(rows)};
     p.C = C; p.K = K; p.silu = activation == CONV_ACT_SILU; p.status = dev.status;
     p.tiles = static_cast<int>(ceil_div(C, conv1d_channels_per_block(K)));
-    const long long blocks = conv_row_blocks(rows, C, K, dev.sms, &p.strip);
+    const long long blocks = conv_row_blocks(rows, C, K, dev.sms, true, &p.strip);
     const long long all = (blocks + (d_state ? nseq : 0)) * p.tiles;
     if (all > kMaxBlocks) return abi_fail(CONV_ERR_UNSUPPORTED, "too many rows and channels for one launch");
     p.row_blocks = static_cast<int>(blocks);
     RETURN_IF(check_workspace(workspace, workspace_bytes, static_cast<size_t>(blocks) * (K + 1) * C * sizeof(float)));
     p.partial = static_cast<float *>(workspace);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (all > 0) RETURN_IF(abi_launch(launch_conv1d_backward(p, elt == 4, wide, s), "causal convolution gradient"));
+    const int box = conv1d_channels_per_block(K), batch = kConvBatch / elt;
+    const bool tma = wide && tile_map(x, x_stride, rows, C, elt, box, batch, &q.in[0]) &&
+                     tile_map(dy, dy_stride, rows, C, elt, box, batch, &q.in[1]) &&
+                     tile_map(dx, dx_stride, rows, C, elt, box, batch, &q.out);
+    if (all > 0) RETURN_IF(abi_launch(launch_conv1d_backward(q, elt == 4, tma, s), "causal convolution gradient"));
     RETURN_IF(abi_launch(launch_conv1d_reduce(p.partial, dw, db, p.row_blocks, C, K, elt == 4, s), "weight gradient sum"));
     return abi_ok();
 }
