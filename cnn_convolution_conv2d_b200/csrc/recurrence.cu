@@ -20,7 +20,8 @@
 // start as all ones bits, which no published value has.
 //
 // Sequence starts inside an item are cuts: there A = 0, and joining selects instead of
-// multiplying, so what a sequence holds (infinities and NaN too) never reaches its neighbour.
+// multiplying, so what a sequence holds (infinities and NaN too) never reaches its neighbour.  Where
+// there is no cut, A is kept above 0, so that a NaN reaches every later row of its sequence.
 //
 // Bound by HBM (8 bytes an element forward, 14 backward in bf16) with the arithmetic close
 // behind: two sigmoids, an exponential and a square root an element.  Hence two channels to an
@@ -193,6 +194,11 @@ __device__ __forceinline__ float2 sigmoid2(float2 z) {
     return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
 
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
 // 2^y - 1 for y <= 0, exact to a few units of the result also where it is small: with
 // y = n + f, |f| <= 1/2, it is 2^n (2^f - 1) + (2^n - 1).  2^f - 1 is f times the polynomial of
 // degree 5 that interpolates (2^f - 1)/f at the Chebyshev points of [-1/2, 1/2] (2e-8 off).
@@ -200,7 +206,7 @@ __device__ __forceinline__ float2 sigmoid2(float2 z) {
 // exponential, biased by a unit or two, would not do.  (No special-function unit is used either:
 // the sigmoids keep that one busy.)
 __device__ __forceinline__ float2 exp2m1(float2 y) {
-    y = make_float2(fmaxf(y.x, -126.f), fmaxf(y.y, -126.f));
+    y = make_float2(max_or_nan(y.x, -126.f), max_or_nan(y.y, -126.f));
     constexpr float kRound = 12582912.f + 127.f;  // 1.5 * 2^23 and the exponent's bias: adding it leaves n + 127 in the low bits
     const float2 r = add2(y, splat(kRound));
     const float2 f = fma2(add2(r, splat(-kRound)), splat(-1.f), y);
@@ -223,6 +229,13 @@ __device__ __forceinline__ float2 contribution(float2 p, float2 rx, float2 x) {
 }
 
 // ------------------------------------------------------------------ joining ---
+// The product of two runs' decays.  Only a cut makes it 0: a product that falls below the smallest number is that
+// number, and of a NaN (which H has too) the smallest number is left.
+constexpr float kLeast = 1.4e-45f;
+__device__ __forceinline__ float product(float A, float B) { return A == 0.f || B == 0.f ? 0.f : fmaxf(A * B, kLeast); }
+__device__ __forceinline__ float2 product(float2 A, float2 B) { return make_float2(product(A.x, B.x), product(A.y, B.y)); }
+__device__ __forceinline__ float2 no_cut(float2 a) { return make_float2(fmaxf(a.x, kLeast), fmaxf(a.y, kLeast)); }
+
 // The state behind a run (A, H) that h enters; a run with a cut (A = 0) forgets h, whatever it is.
 __device__ __forceinline__ float after(float A, float H, float h) { return A == 0.f ? H : fmaf(A, h, H); }
 
@@ -361,7 +374,7 @@ __device__ __forceinline__ bool exchange(Joins<W, kBack> &s, float4 run, int war
 // Joins a run (A0, H0, A1, H1) to what lies in front of it; without a cut in the chunk a product will do.
 template <bool kEdge>
 __device__ __forceinline__ float4 join(float4 all, float4 r) {
-    if (kEdge) return make_float4(all.x * r.x, after(r.x, r.y, all.y), all.z * r.z, after(r.z, r.w, all.w));
+    if (kEdge) return make_float4(product(all.x, r.x), after(r.x, r.y, all.y), product(all.z, r.z), after(r.z, r.w, all.w));
     const float2 A = make_float2(r.x, r.z), H = fma2(A, make_float2(all.y, all.w), make_float2(r.y, r.w));
     const float2 P = mul2(make_float2(all.x, all.z), A);
     return make_float4(P.x, H.x, P.y, H.y);
@@ -388,6 +401,10 @@ __device__ __forceinline__ void join_runs(const RecParams &p, int chunk, bool ne
     if (sends) {
 #pragma unroll
         for (int i = 0; i < W; ++i) all = join<kEdge>(all, runs[kForward ? i : W - 1 - i][lane]);
+        if (!kEdge) {
+            all.x = fmaxf(all.x, kLeast);
+            all.z = fmaxf(all.z, kLeast);
+        }
         if (needed) {
             publish(p.aggregate + at + l.c0, all.x, all.y);
             publish(p.aggregate + at + l.c1, all.z, all.w);
@@ -444,7 +461,8 @@ __device__ __forceinline__ bool forward_item(const RecParams &p, Rows &rows, con
             A[j] = splat(0.f);
             H[j] = fma2(a, load_f32(seq_row(p.state, run, j, p.C), rows.l), b);
         } else {
-            A[j] = j ? mul2(A[j ? j - 1 : 0], a) : a;
+            if (kEdge) A[j] = j ? product(A[j ? j - 1 : 0], no_cut(a)) : no_cut(a);
+            else A[j] = j ? mul2(A[j ? j - 1 : 0], a) : a;
             H[j] = j ? fma2(a, H[j ? j - 1 : 0], b) : b;
         }
     }
@@ -515,7 +533,7 @@ __device__ __forceinline__ bool backward_item(const RecParams &p, Rows &rows, co
             g = j < L - 1 ? fma2(a, g, dh) : dh;
         }
         a = add1(pm[j], 1.f);
-        B = mul2(B, a);
+        B = kEdge ? product(B, no_cut(a)) : mul2(B, a);
     }
     const float2 S = mul2(a, g);
     if (!exchange(s, make_float4(B.x, S.x, B.y, S.y), warp)) return false;

@@ -274,6 +274,44 @@ def test_what_one_sequence_holds_stays_there(poison, dtype):
 
 
 @both
+@pytest.mark.parametrize("offsets", [None, [0, 3, 400, 600]], ids=["dense", "packed"])
+@pytest.mark.parametrize("decay", [-3.5, 3.0], ids=["slow", "fast"])
+def test_nan_reaches_the_later_rows_of_its_sequence(decay, offsets, dtype):
+    """A NaN in any input of a row makes every later state of its sequence NaN, however small the decays' products;
+    one in dy every earlier gradient.  Infinities leave no finite state either."""
+    d = Draw(12, dtype)
+    C, rows, at, first, last = 64, 600, 77, 3 if offsets else 0, 400 if offsets else 600
+    x, ga, gx, dy = (d(rows, C)[0] if offsets else d(1, rows, C)[0] for _ in range(4))
+    rec, off = cb.GatedRecurrenceB200(torch.full((C,), decay, device="cuda")), dev(offsets)
+    flat = lambda t: t.view(rows, C)  # noqa: E731
+    for which, bad in [(i, float("nan")) for i in range(3)] + [(0, float("inf"))]:
+        t = [v.clone() for v in (x, ga, gx)]
+        flat(t[which])[at, 5] = bad
+        y = flat(rec(*t, offsets=off))
+        assert not bool(y[at:last, 5].isfinite().any())
+        if bad != bad:
+            assert bool(y[at:last, 5].isnan().all())
+        y[at:last, 5] = 0
+        assert bool(y.isfinite().all())
+    state = torch.zeros(len(offsets) - 1 if offsets else 1, C, device="cuda")
+    state[1 if offsets else 0, 5] = float("nan")
+    y = flat(rec(x, ga, gx, offsets=off, initial_state=state))
+    assert bool(y[first:last, 5].isnan().all())
+    y[first:last, 5] = 0
+    assert bool(y.isfinite().all())
+    saved = rec.saved_states(x)
+    rec(x, ga, gx, offsets=off, saved=saved)
+    bad = dy.clone()
+    flat(bad)[at, 5] = float("nan")
+    for g in rec.backward(x, ga, gx, bad, saved, offsets=off)[:3]:
+        g = flat(g)
+        assert bool(g[first:at + 1, 5].isnan().all())
+        g[first:at + 1, 5] = 0
+        assert bool(g.isfinite().all())
+    cb.conv2d_sync_status()
+
+
+@both
 def test_masked_gates_keep_the_state(dtype):
     """gate_a of the lowest value or -infinity: the row adds nothing, has no gradient, and the state passes."""
     C, T = 64, 200
