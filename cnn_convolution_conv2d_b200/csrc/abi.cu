@@ -2062,6 +2062,7 @@ int conv2d_sync_status(conv_stream_t stream) {
         if (v == kDevBadOffsets)
             return fail(CONV_ERR_INVALID_ARG, "sequence offsets must begin at 0, never fall and end inside the rows");
         if (v == kDevBadSlot) return fail(CONV_ERR_INVALID_ARG, "two rows of a step named the same slot");
+        if (v == kDevBadStep) return fail(CONV_ERR_INVALID_ARG, "the number of an optimizer's step was below 1");
         return fail(CONV_ERR_TIMEOUT, "device watchdog fired (code %d)", v);
     }
     return ok();

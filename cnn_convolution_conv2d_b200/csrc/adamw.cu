@@ -3,13 +3,13 @@
 //   g = grad scale, m = b1 m + (1-b1) g, v = b2 v + (1-b2) g^2,
 //   p = p (1 - lr wd) - lr m / (1-b1^t) / (sqrt(v / (1-b2^t)) + eps)
 //
-// With 32-bit states bound by HBM (28 bytes an element, 6.6 TB/s); with 8-bit states by the issue of
+// With 32-bit states bound by HBM (28 bytes an element, 6.7 TB/s); with 8-bit states by the issue of
 // instructions, about 70 for an element's 10 bytes: a third of them the random bits and the rounding.  So there a thread
 // keeps to 40 registers, for 48 warps an SM, and a block takes several batches of 1024 elements of one tensor, which it
 // finds by a search in the table of tensors.  The table is a kernel argument: nothing is uploaded, and a captured
 // launch keeps its own copy.  Every element is read and written once.
-// 100 M elements: fp32 420 us (6.7 TB/s); bf16 with fp32 master weights 420 us, with 8-bit states 258 us (3.9 TB/s),
-// with both 297 us (5.4 TB/s).
+// 100 M elements: fp32 414 us (6.8 TB/s); bf16 with fp32 master weights 418 us, with 8-bit states 266 us (3.8 TB/s),
+// with both 303 us (5.3 TB/s).
 //
 // 8-bit states hold 256 elements (a warp's) to one scale, a power of two, so that scaling is
 // exact: m in e4m3 (largest element in [2^7, 2^8)), v in e5m2 ([2^14, 2^15): v spans twice the
@@ -29,9 +29,10 @@ namespace {
 
 constexpr int E = kAdamPerThread;
 
+// (With numbers below 2^-126: where eps is 0 or near it, such a v counts.  8 of the 266 us above.)
 __device__ __forceinline__ float sqrt_approx(float x) {
     float y;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -162,6 +163,10 @@ __global__ void __launch_bounds__(kAdamThreads, kEight ? 12 : 1) adamw_kernel(co
     long long step = q.step;
     if (q.step_device) {  // 1 - beta^step in 64 bits: it is small for the first steps
         step = *q.step_device;
+        if (step < 1) {
+            if (blockIdx.x == 0 && threadIdx.x == 0) atomicExch(q.status, kDevBadStep);
+            return;
+        }
         if (threadIdx.x == 0) {
             s_rate[0] = static_cast<float>(q.lr / -expm1(static_cast<double>(step) * q.ln_beta1));
             s_rate[1] = static_cast<float>(1.0 / sqrt(-expm1(static_cast<double>(step) * q.ln_beta2)));

@@ -36,6 +36,7 @@ struct AdamParams {
     const long long *step_device;
     const float *grad_scale;
     unsigned seed;
+    int *status;
 };
 
 cudaError_t launch_adamw(const AdamParams &p, bool p32, bool g32, bool master, bool eight, cudaStream_t s);

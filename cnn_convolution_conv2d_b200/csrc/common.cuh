@@ -27,6 +27,7 @@ enum DeviceStatus : int {
     kDevTimeoutCarry = 7,    // a chunk of a recurrence waited too long for the one before it
     kDevBadOffsets = 8,      // sequence offsets fall, or leave the rows
     kDevBadSlot = 9,         // two rows of a step name the same slot (the later one was skipped)
+    kDevBadStep = 10,        // the number of an optimizer's step is below 1
 };
 
 // Everything one launch of the implicit-GEMM kernel needs.  Rows of the

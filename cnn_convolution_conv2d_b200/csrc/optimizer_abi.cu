@@ -101,6 +101,7 @@ int adamw_step(const adamw_tensor_t *tensors, int count, conv_dtype_t param_dtyp
     p.step_device = step_device;
     p.grad_scale = grad_scale;
     p.seed = seed;
+    p.status = dev.status;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // With 8-bit states a block takes more batches, and finds its tensor once for them, where that leaves 8 blocks an SM
     // (100 M elements: 313 -> 258 us); with 32-bit states, which wait for memory alone, that costs (422 -> 438 us).

@@ -38,7 +38,8 @@ class AdamWB200:
     ``state_bits``: 32 (fp32 states) or 8 (e4m3 and e5m2 codes with a power of two for each 256 elements, rounded by
     chance from ``seed``).  ``masters``: for bf16 weights, None (the weights themselves are updated, rounded to nearest),
     True (fp32 copies are made), or a list of fp32 tensors.  ``step_device``: an int64 CUDA tensor of one element that
-    holds the number of the step to come, for steps captured into a graph; the caller counts it up.  Otherwise
+    holds the number of the step to come, for steps captured into a graph; the caller counts it up (below 1 a
+    step changes nothing, and ``conv2d_sync_status`` reports it).  Otherwise
     ``step_count`` counts the steps taken.
 
     The states lie in one buffer each, a tensor at a multiple of 256 elements: ``flat["m"]``, ``flat["v"]`` and, with 8
@@ -107,7 +108,7 @@ class AdamWB200:
     def step(self, grads, lr=None, grad_scale=None, stream=None):
         """One step with ``grads``, a gradient (bf16 or fp32, one dtype) for each weight.  ``grad_scale``: a
         one-element fp32 CUDA tensor that multiplies them; where it is not finite or not above zero nothing
-        changes.  ``lr``: this step's rate instead of the optimizer's."""
+        changes (the step is counted all the same).  ``lr``: this step's rate instead of the optimizer's."""
         import torch
         if len(grads) != len(self.params):
             raise ValueError(f"{len(self.params)} gradients are wanted, {len(grads)} given")

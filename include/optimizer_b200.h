@@ -42,7 +42,8 @@ typedef struct {
  * tensors must not overlap.  Either all or none have master weights.
  *   step        : the step's number, 1 for the first; ignored where step_device is given
  *   step_device : NULL, or a device integer with that number, read when the kernel runs (for
- *                 a captured step, whose graph counts it up before each replay)
+ *                 a captured step, whose graph counts it up before each replay).  Below 1 the step changes nothing
+ *                 and conv2d_sync_status reports CONV_ERR_INVALID_ARG.
  *   grad_scale  : NULL (1), or a device float that multiplies the gradients (the reciprocal
  *                 of a loss scale, a clipping coefficient).  Where it is not finite or not
  *                 above zero the step changes nothing.

@@ -170,6 +170,34 @@ def test_what_is_not_finite(bits):
     assert bool(opt.exp_avg[0].float()[mask].isfinite().all()) and bool(opt.exp_avg_sq[0].float()[mask].isfinite().all())
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_small_gradients_count_without_eps(bits):
+    """g near 1e-18, so v near 1e-39, below the smallest normal number: m^ / sqrt(v^) is still 1 in size after one step.
+    v's products are off by half a unit of 2^-149 each, 7e-7 of the smallest v here: 2e-6 of the update is wide."""
+    p, g = normal((999,), 1, 0.1), (normal((999,), 2).abs() + 1) * 1e-18
+    p0 = p.double()
+    opt = cb.AdamWB200([p], lr=1e-2, eps=0.0, weight_decay=0.0, state_bits=bits)
+    opt.step([g])
+    want = p0 - 1e-2
+    assert bool(((p.double() - want).abs() <= 2 * ref.U * p0.abs() + 1e-2 * (2e-6 + 16 * ref.U)).all())
+
+
+def test_a_step_number_below_one_is_reported():
+    p = normal((300,), 1)
+    kept = p.clone()
+    counter = torch.zeros(1, dtype=torch.int64, device="cuda")
+    opt = cb.AdamWB200([p], step_device=counter)
+    opt.step([normal((300,), 2)])
+    with pytest.raises(cb.Conv2dError) as err:
+        cb.conv2d_sync_status()
+    assert err.value.status == cb.CONV_ERR_INVALID_ARG and "step" in str(err.value)
+    assert torch.equal(p, kept) and bool((opt.flat["m"] == 0).all())
+    counter += 1
+    opt.step([normal((300,), 2)])
+    cb.conv2d_sync_status()
+    assert not torch.equal(p, kept)
+
+
 def test_refusals():
     p = [torch.zeros(16, device="cuda"), torch.zeros(16, device="cuda")]
     for bad in (lambda: cb.AdamWB200([p[0], p[0]]), lambda: cb.AdamWB200([p[0], p[0][4:12]]), lambda: cb.AdamWB200(p, state_bits=4),
