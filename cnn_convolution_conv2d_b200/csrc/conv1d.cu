@@ -57,7 +57,7 @@ __device__ __forceinline__ void copy_ahead(Raw<T, V> *to, const T *row, const Ch
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (ch.has(v)) ptx::cp_async_4(&to->v[v], row + ch.at(v));
+            if (ch.has(v)) cp_async_4(&to->v[v], row + ch.at(v));
     } else {
         *to = load_raw<T, V, false>(row, ch);
     }
@@ -97,7 +97,7 @@ struct Ring {
                     for (int i = 0; i < N; ++i)
                         copy_ahead<T, V>(&rows[to][i][u][threadIdx.x & 31], from[i] + static_cast<size_t>(row + u) * ld[i], ch);
                 }
-            ptx::cp_async_commit();
+            cp_async_commit();
         }
     }
     __device__ __forceinline__ bool wait(const Conv1dParams &p) {
@@ -105,7 +105,7 @@ struct Ring {
             const ptx::Watchdog wd{abort, p.status, static_cast<uint64_t>(p.timeout_ns)};
             if (!ptx::mbar_wait(&full[slot], parity, wd, kDevTimeoutFull)) return false;
         } else {
-            ptx::cp_async_wait<1>();
+            cp_async_wait<1>();
         }
         --coming;
         return true;

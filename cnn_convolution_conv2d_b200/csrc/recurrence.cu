@@ -366,7 +366,7 @@ template <int W, bool kBack>
 __device__ __forceinline__ bool exchange(Joins<W, kBack> &s, float4 run, int warp) {
     s.run[warp][threadIdx.x & 31] = run;
     __syncwarp();
-    ptx::named_barrier_arrive(kRunsIn, (W + 1) * 32);
+    named_barrier_arrive(kRunsIn, (W + 1) * 32);
     ptx::named_barrier(kStartsIn, (W + 1) * 32);
     return *static_cast<volatile int *>(&s.stop) == 0;
 }
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 2) rec_plain_kernel(const __grid
         if (warp == W) {
             ptx::named_barrier(kRunsIn, (W + 1) * 32);
             join_item<W, L, kBack>(p, item, s.run, s.start, rows.l);
-            ptx::named_barrier_arrive(kStartsIn, (W + 1) * 32);
+            named_barrier_arrive(kStartsIn, (W + 1) * 32);
         } else if (item.flags & kEdges) {
             work_item_edges<W, kBack>(p, rows, run_of<L>(p.seq, row0, chunk_limit(p, item.chunk)), s, s.sum[0], warp, nothing);
         } else {
@@ -760,7 +760,7 @@ __global__ void __launch_bounds__((W + 1) * 32, kBlocks) rec_tile_kernel(const _
             if (stop) s.stop = 1;
             else join_item<W, L, kBack>(p, item, s.run, s.start, l);
             __syncwarp();
-            ptx::named_barrier_arrive(kStartsIn, kAll);
+            named_barrier_arrive(kStartsIn, kAll);
             if (stop) break;
             if constexpr (kBack) {
                 if (one.x >= 0) store_sum<W>(p, one.x, s.sum[~n & 1], Lane2<true>(one.y, p.C));

@@ -8,9 +8,10 @@
  *
  * - A tensor over sequences is a matrix of `rows` rows of C channels.  Channels are
  *   contiguous; rows lie `*_stride` elements apart (at least C for what is written; 0 is
- *   allowed for what is read).  Pointers need the alignment of their element only; rows
- *   whose pointer, stride and C are multiples of 4 channels (convolution; 2 where K > 4)
- *   or 2 channels (recurrence) are read and written with wide accesses.
+ *   allowed for what is read).  Pointers need the alignment of their element only.  Fastest
+ *   are tensors whose pointers and row strides are all multiples of 16 bytes (for the
+ *   convolution C and the states' pointers multiples of 4 channels too, 2 where K > 4);
+ *   others take up to twice the time.
  * - offsets = NULL: the rows are nseq sequences of T rows, rows = nseq * T.  Otherwise
  *   offsets holds nseq + 1 device ints, offsets[0] = 0, never falling, at most `rows`:
  *   sequence s has rows offsets[s] .. offsets[s+1]-1 (it may be empty) and T is ignored.
@@ -18,6 +19,8 @@
  *   result and no output row is written there.  Offsets that break the rule are reported
  *   as CONV_ERR_INVALID_ARG by conv2d_sync_status (the results are then undefined).
  * - A sequence sees only its own rows: infinities and NaN of one never reach another.
+ *   Inside it a NaN in a row of the recurrence reaches every later state; an infinite state
+ *   leaves infinities or NaN.
  * - Results do not depend on timing: equal inputs give equal bits.
  * - Outputs must not overlap inputs or each other; rows may interleave in one buffer.
  * - rows = 0 is allowed (tensors over rows may then be NULL), nseq = 0 is not.
