@@ -388,15 +388,13 @@ __device__ __forceinline__ float2 step_over(float4 r, float2 h) {
 // The joining warp's part of an item: publishes the chunk's (A, H), finds the state that enters the chunk,
 // publishes the one that leaves it, and hands out those that enter the runs.
 template <bool kEdge, bool kForward, int W, bool kAdjacent>
-__device__ __forceinline__ void join_runs(const RecParams &p, int chunk, bool needed, const float4 (*runs)[32],
-                                          float2 (*start)[32], const Lane2<kAdjacent> &l) {
+__device__ __forceinline__ void join_runs(const RecParams &p, int chunk, bool needed, Published<kAdjacent> &front,
+                                          const float4 (*runs)[32], float2 (*start)[32], const Lane2<kAdjacent> &l) {
     constexpr int kStep = kForward ? 1 : -1;
     const int lane = threadIdx.x & 31;
     const int before = kForward ? chunk : p.chunks - 1 - chunk;
     const bool sends = (kForward ? chunk + 1 < p.chunks : chunk > 0) && !p.starve;
     const size_t at = static_cast<size_t>(chunk) * p.Cpad;
-    Published<kAdjacent> front;
-    if (needed) front.read(p, chunk, before, kStep, l);
     float4 all = make_float4(1.f, 0.f, 1.f, 0.f);
     if (sends) {
 #pragma unroll
@@ -639,25 +637,30 @@ __device__ __forceinline__ Item item_of(const RecParams &p, unsigned item, int c
     return Item{chunk, tile, row0, saved_place(p, chunk, row0), (has_edges(p.seq, row0, chunk_rows) ? kEdges : 0) | (item == 0 ? kFirst : 0)};
 }
 
-// The joining warp's work on an item.
+// The joining warp's work on an item: first, while the runs are still at work, it looks for what is in front.
 template <int W, int L, bool kBack, bool kAdjacent>
-__device__ __forceinline__ void join_item(const RecParams &p, const Item &item, const float4 (*runs)[32], float2 (*start)[32],
-                                          const Lane2<kAdjacent> &l) {
-    const int chunk = item.chunk;
-    // whether the rows in front of the chunk (against the order of time: behind it) reach into it
-    bool needed = kBack ? chunk + 1 < p.chunks : chunk > 0;
-    if (!(item.flags & kEdges)) {
-        join_runs<false, !kBack, W>(p, chunk, needed, runs, start, l);
-        return;
+struct Joining {
+    Published<kAdjacent> front;
+    bool needed;  // whether the rows in front of the chunk (against the order of time: behind it) reach into it
+    __device__ __forceinline__ void look(const RecParams &p, const Item &item, const Lane2<kAdjacent> &l) {
+        const int chunk = item.chunk;
+        needed = kBack ? chunk + 1 < p.chunks : chunk > 0;
+        if (item.flags & kEdges) {
+            if (p.per_seq) {
+                needed = (kBack ? chunk + 1 : chunk) % p.per_seq != 0;
+            } else if (needed) {
+                const int row0 = item.row0, row1 = row0 + W * L, s = seq_of(p.seq, kBack ? row1 - 1 : row0);
+                needed = s >= 0 && (kBack ? row1 < seq_begin(p.seq, s + 1) : seq_begin(p.seq, s) < row0 && row0 < seq_begin(p.seq, s + 1));
+            }
+        }
+        if (needed) front.read(p, chunk, kBack ? p.chunks - 1 - chunk : chunk, kBack ? -1 : 1, l);
     }
-    if (p.per_seq) {
-        needed = (kBack ? chunk + 1 : chunk) % p.per_seq != 0;
-    } else if (needed) {
-        const int row0 = item.row0, row1 = row0 + W * L, s = seq_of(p.seq, kBack ? row1 - 1 : row0);
-        needed = s >= 0 && (kBack ? row1 < seq_begin(p.seq, s + 1) : seq_begin(p.seq, s) < row0 && row0 < seq_begin(p.seq, s + 1));
+    __device__ __forceinline__ void join(const RecParams &p, const Item &item, const float4 (*runs)[32], float2 (*start)[32],
+                                         const Lane2<kAdjacent> &l) {
+        if (item.flags & kEdges) join_runs<true, !kBack, W>(p, item.chunk, needed, front, runs, start, l);
+        else join_runs<false, !kBack, W>(p, item.chunk, needed, front, runs, start, l);
     }
-    join_runs<true, !kBack, W>(p, chunk, needed, runs, start, l);
-}
+};
 
 // Items element by element, for tensors that TMA does not take.
 template <typename T, int W, int L, bool kBack>
@@ -680,8 +683,10 @@ __global__ void __launch_bounds__((W + 1) * 32, 2) rec_plain_kernel(const __grid
             copy_empty<W + 1>(p.seq, kBack ? p.d_final : p.state, kBack ? p.d_state : p.final_state, p.C, rows.l);
         auto nothing = [] {};
         if (warp == W) {
+            Joining<W, L, kBack, false> joining;
+            joining.look(p, item, rows.l);
             ptx::named_barrier(kRunsIn, (W + 1) * 32);
-            join_item<W, L, kBack>(p, item, s.run, s.start, rows.l);
+            joining.join(p, item, s.run, s.start, rows.l);
             named_barrier_arrive(kStartsIn, (W + 1) * 32);
         } else if (item.flags & kEdges) {
             work_item_edges<W, kBack>(p, rows, run_of<L>(p.seq, row0, chunk_limit(p, item.chunk)), s, s.sum[0], warp, nothing);
@@ -755,10 +760,12 @@ __global__ void __launch_bounds__((W + 1) * 32, kBlocks) rec_tile_kernel(const _
             if (item.flags & kFirst) check_offsets(p.seq, p.status, lane, 32);
             ptx::mbar_wait(&s_free, n & 1u, wd, kDevTimeoutEmpty);
             if (n > 0) issue((n - 1) % S);
+            Joining<W, L, kBack, true> joining;
+            joining.look(p, item, l);
             ptx::named_barrier(kRunsIn, kAll);
             stop = *static_cast<volatile int *>(&s_abort) != 0;
             if (stop) s.stop = 1;
-            else join_item<W, L, kBack>(p, item, s.run, s.start, l);
+            else joining.join(p, item, s.run, s.start, l);
             __syncwarp();
             named_barrier_arrive(kStartsIn, kAll);
             if (stop) break;
