@@ -67,111 +67,114 @@ __device__ __forceinline__ float2 one_minus(float2 a) { return fma2(a, splat(-1.
 __device__ __forceinline__ float2 negative(float2 a) { return make_float2(-a.x, -a.y); }
 
 // ----------------------------------------------------------- element access ---
-// The two channels of a lane: adjacent, or 32 apart.
-template <bool kAdjacent>
+// Half a warp (16 lanes) takes the channels of a tile, and the two halves of a warp take runs of their own.
+__device__ __forceinline__ int lane16() { return threadIdx.x & 15; }
+__device__ __forceinline__ int half() { return threadIdx.x >> 4 & 1; }
+
+// The two channels of a lane: of a tile, adjacent ones.
 struct Lane2 {
     int c0, c1;
     bool ok0, ok1;
-    __device__ Lane2(int tile, int C) {
-        const int lane = threadIdx.x & 31;
-        c0 = tile * kRecTile + (kAdjacent ? 2 * lane : lane);
-        c1 = c0 + (kAdjacent ? 1 : 32);
-        ok0 = c0 < C;
-        ok1 = c1 < C;
-    }
+    __device__ Lane2(int c0_, int c1_, int C) : c0(c0_), c1(c1_), ok0(c0_ < C), ok1(c1_ < C) {}
+    __device__ Lane2(int tile, int C) : Lane2(tile * kRecTile + 2 * lane16(), tile * kRecTile + 2 * lane16() + 1, C) {}
 };
 
-template <typename T, bool kAdjacent>
-__device__ __forceinline__ float2 load2(const T *row, const Lane2<kAdjacent> &l) {
+template <typename T>
+__device__ __forceinline__ float2 load2(const T *row, const Lane2 &l) {
     return make_float2(l.ok0 ? to_float(row[l.c0]) : 0.f, l.ok1 ? to_float(row[l.c1]) : 0.f);
 }
-template <typename T, bool kAdjacent>
-__device__ __forceinline__ void store2(T *row, float2 f, const Lane2<kAdjacent> &l) {
+template <typename T>
+__device__ __forceinline__ void store2(T *row, float2 f, const Lane2 &l) {
     if (l.ok0) row[l.c0] = from_float<T>(f.x);
     if (l.ok1) row[l.c1] = from_float<T>(f.y);
 }
-template <bool kAdjacent>
-__device__ __forceinline__ float2 load_f32(const float *row, const Lane2<kAdjacent> &l) {
+__device__ __forceinline__ float2 load_f32(const float *row, const Lane2 &l) {
     return row ? load2<float>(row, l) : make_float2(0.f, 0.f);
 }
 
 // The tensors of an item, by their place in its tile.
 enum : int { kX = 0, kGateA = 1, kGateX = 2, kDy = 3 };
 
-// The rows of one warp's run in global memory, element by element.
-template <typename T, int L>
-struct GlobalRun {
-    static constexpr int kRun = L;
-    static constexpr bool kAdjacent = false;
-    const T *in[4];
-    T *out[3];
-    long long ld[4], ldo[3];
-    int saved;  // the place of its first saved state
-    Lane2<false> l;
-    __device__ GlobalRun(const RecParams &p, int tile, int row0, int saved_) : saved(saved_), l(tile, p.C) {
-        const void *from[4] = {p.x, p.ga, p.gx, p.dy};
-        void *to[3] = {p.y, p.dga, p.dgx};
-        const long long lf[4] = {p.ldx, p.lda, p.ldg, p.lddy}, lt[3] = {p.ldy, p.ld_da, p.ld_dg};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            ld[i] = lf[i];
-            in[i] = static_cast<const T *>(from[i]) + static_cast<size_t>(row0) * lf[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            ldo[i] = lt[i];
-            out[i] = static_cast<T *>(to[i]) + static_cast<size_t>(row0) * lt[i];
-        }
-    }
-    __device__ float2 get(int tensor, int j) const { return load2<T>(in[tensor] + j * ld[tensor], l); }
-    __device__ void put(int tensor, int j, float2 f) { store2<T>(out[tensor] + j * ldo[tensor], f, l); }
-    __device__ void done(int) {}
-};
-
-// The rows of one warp's run in a tile in shared memory, where the results take the places of the
-// inputs (same tensor, same thread) and leave by one bulk store each -- unless some rows of
-// the run belong to no sequence: those must not be written, so the others go out one by one.
-template <typename T, int kRows, int L>
+// The rows of a half warp's run in a tile in shared memory, where the results take the places of the
+// inputs (same tensor, same thread).  By TMA they leave by one bulk store for a warp and tensor -- unless some rows of
+// the warp's runs belong to no sequence: those must not be written, so the others go out one by one.  Otherwise
+// the warp copies its rows in and out itself, a lane a channel.
+// (In bf16 the two halves meet in the same 16 banks: their rows lie an even number of 64 bytes apart.)
+template <typename T, int kRows, int L, bool kTma>
 struct TileRun {
-    static constexpr int kRun = L;
-    static constexpr bool kAdjacent = true;
+    static constexpr int kRun = L, kTwo = 2 * L;
     static constexpr int kRow = kRecTile * sizeof(T), kTensor = kRows * kRow;
-    uint8_t *base;   // this warp's first row
-    const CUtensorMap *maps;  // of the outputs, boxes of L rows
+    static constexpr unsigned kAll = ~0u >> (32 - kTwo);
     const RecParams &p;
-    int tile, row0, saved;
-    bool whole;
-    Lane2<true> l;
-    __device__ TileRun(const RecParams &p_, const CUtensorMap *maps_, uint8_t *stage, int tile_, int row0_, int saved_, int warp, bool whole_)
-        : base(stage + warp * L * kRow), maps(maps_), p(p_), tile(tile_), row0(row0_), saved(saved_), whole(whole_), l(tile_, p_.C) {}
+    const CUtensorMap *maps;  // of the outputs, boxes of 2 L rows
+    uint8_t *first;  // the warp's first row
+    uint8_t *base;   // this half's
+    int tile, row0, saved;  // row0: the warp's first row
+    unsigned present;       // a bit for each of the warp's rows: it belongs to a sequence
+    Lane2 l;
+    __device__ TileRun(const RecParams &p_, const CUtensorMap *maps_, uint8_t *stage, int warp, int tile_, int row0_, int saved_)
+        : p(p_), maps(maps_), first(stage + warp * kTwo * kRow), base(first + half() * L * kRow), tile(tile_), row0(row0_),
+          saved(saved_), present(kAll), l(tile_, p_.C) {}
     __device__ uint8_t *at(int tensor, int j) const {
-        return base + tensor * kTensor + j * kRow + (threadIdx.x & 31) * 2 * static_cast<int>(sizeof(T));
+        return base + tensor * kTensor + j * kRow + lane16() * 2 * static_cast<int>(sizeof(T));
     }
+    __device__ T *output(int tensor) const { return static_cast<T *>(tensor == 0 ? p.y : tensor == 1 ? p.dga : p.dgx); }
+    __device__ long long stride(int tensor) const { return tensor == 0 ? p.ldy : tensor == 1 ? p.ld_da : p.ld_dg; }
     __device__ float2 get(int tensor, int j) const {
         if constexpr (sizeof(T) == 4) return *reinterpret_cast<const float2 *>(at(tensor, j));
         const uint32_t v = *reinterpret_cast<const uint32_t *>(at(tensor, j));
         return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
     }
     __device__ void put(int tensor, int j, float2 f) {
-        if (!whole) {
-            T *out = static_cast<T *>(tensor == 0 ? p.y : tensor == 1 ? p.dga : p.dgx);
-            const long long ld = tensor == 0 ? p.ldy : tensor == 1 ? p.ld_da : p.ld_dg;
-            store2<T>(out + static_cast<size_t>(row0 + j) * ld, f, l);
+        if (kTma && present != kAll) {
+            store2<T>(output(tensor) + static_cast<size_t>(row0 + half() * L + j) * stride(tensor), f, l);
         } else if constexpr (sizeof(T) == 4) {
             *reinterpret_cast<float2 *>(at(tensor, j)) = f;
         } else {
             *reinterpret_cast<__nv_bfloat162 *>(at(tensor, j)) = __float22bfloat162_rn(f);
         }
     }
-    // Sends the results of the first n tensors; the tile is free once lane 0's bulk reads are done.
+    // Sends the results of the first n tensors; by TMA, the tile is free once lane 0's bulk reads are done.
     __device__ void done(int n) {
-        if (!whole) return;
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) {
-            for (int i = 0; i < n; ++i) ptx::tma_store_2d(maps + i, base + i * kTensor, tile * kRecTile, row0);
-            ptx::bulk_commit_group();
+        if constexpr (kTma) {
+            if (present != kAll) return;
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) {
+                for (int i = 0; i < n; ++i) ptx::tma_store_2d(maps + i, first + i * kTensor, tile * kRecTile, row0);
+                ptx::bulk_commit_group();
+            }
+        } else {
+            __syncwarp();
+            const int lane = threadIdx.x & 31, c = tile * kRecTile + lane;
+            for (int i = 0; i < n; ++i) {
+                T *out = output(i) + static_cast<size_t>(row0) * stride(i) + c;
+                const T *from = reinterpret_cast<const T *>(first + i * kTensor) + lane;
+#pragma unroll 8
+                for (int r = 0; r < kTwo; ++r)
+                    if ((present >> r & 1u) && c < p.C) out[r * stride(i)] = from[r * kRecTile];
+            }
+            __syncwarp();
         }
+    }
+    // Copies the warp's rows of the first n tensors in, asynchronously where the copy instruction has the size (4 bytes).
+    __device__ void fetch(int n) {
+        const int lane = threadIdx.x & 31, c = tile * kRecTile + lane, rows = min(p.seq.rows - row0, kTwo);
+        for (int i = 0; i < n; ++i) {
+            const long long ld = i == kX ? p.ldx : i == kGateA ? p.lda : i == kGateX ? p.ldg : p.lddy;
+            const T *from = static_cast<const T *>(i == kX ? p.x : i == kGateA ? p.ga : i == kGateX ? p.gx : p.dy) +
+                            static_cast<size_t>(row0) * ld + c;
+            T *to = reinterpret_cast<T *>(first + i * kTensor) + lane;
+            if (c >= p.C) continue;
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll 4
+                for (int r = 0; r < rows; ++r) cp_async_4(to + r * kRecTile, from + r * ld);
+            } else {
+#pragma unroll 8
+                for (int r = 0; r < rows; ++r) to[r * kRecTile] = from[r * ld];
+            }
+        }
+        cp_async_commit();
     }
 };
 
@@ -181,8 +184,7 @@ __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1
 // log2(a) per unit of ra: -kappa softplus(decay) log2(e).
 __device__ __forceinline__ float decay_rate(float decay, float kappa) { return -kappa * kLog2e * softplus(decay); }
 
-template <bool kAdjacent>
-__device__ __forceinline__ float2 decay_rate(const RecParams &p, const Lane2<kAdjacent> &l) {
+__device__ __forceinline__ float2 decay_rate(const RecParams &p, const Lane2 &l) {
     if (p.rates) return load2<float>(p.rates, l);
     const float2 d = load2<float>(p.decay, l);
     return make_float2(decay_rate(d.x, p.kappa), decay_rate(d.y, p.kappa));
@@ -261,12 +263,11 @@ __device__ __forceinline__ uint64_t peek(const float2 *at) {
 
 // What the chunks in front of a chunk have published, read by one warp: the nearest kWindow ones.
 constexpr int kWindow = 3;
-template <bool kAdjacent>
 struct Published {
     uint64_t a0[kWindow], a1[kWindow];
     uint32_t c0[kWindow], c1[kWindow];
     // step: +1 where the chunk in front of chunk k is k-1, -1 where it is k+1; `before` of them exist
-    __device__ __forceinline__ void read(const RecParams &p, int chunk, int before, int step, const Lane2<kAdjacent> &l) {
+    __device__ __forceinline__ void read(const RecParams &p, int chunk, int before, int step, const Lane2 &l) {
 #pragma unroll
         for (int i = 0; i < kWindow; ++i) {
             a0[i] = a1[i] = 0;
@@ -302,7 +303,8 @@ struct Published {
     }
 };
 
-// What the rows of a run are, a bit each; `seq` of lane j is row j's sequence.
+// What the rows of a half warp's run are, a bit each; `seq` of lane j is the sequence of the warp's row j.  In a chunk
+// of one sequence: whether the run begins or ends it, and the sequence.
 struct Run {
     unsigned in, start, end;
     int seq;
@@ -313,7 +315,7 @@ __device__ __forceinline__ Run run_of(const Sequences &q, int row0, int limit) {
     Run r;
     r.seq = 0;
     bool in = false, start = false, end = false;
-    if (lane < L && row < limit) {
+    if (lane < 2 * L && row < limit) {
         const int s = seq_of(q, row);
         if (s >= 0) {
             const int b = seq_begin(q, s), e = seq_begin(q, s + 1);
@@ -323,21 +325,17 @@ __device__ __forceinline__ Run run_of(const Sequences &q, int row0, int limit) {
             r.seq = s;
         }
     }
-    r.in = __ballot_sync(kFull, in);
-    r.start = __ballot_sync(kFull, start);
-    r.end = __ballot_sync(kFull, end);
+    const auto bits = [](bool v) { return __ballot_sync(kFull, v) >> (half() * L) & ((1u << L) - 1u); };
+    r.in = bits(in);
+    r.start = bits(start);
+    r.end = bits(end);
     return r;
 }
 
-// Whether a sequence begins or ends inside a chunk, or rows of it belong to none: then its rows are looked at one by
-// one.
-__device__ __forceinline__ bool has_edges(const Sequences &q, int row0, int rows) {
-    const int s = seq_of(q, row0);
-    return s < 0 || seq_begin(q, s) >= row0 || seq_begin(q, s + 1) <= row0 + rows;
-}
-
+// The channels of the sequence of a run's row j.  Called by the whole warp.
+template <int L>
 __device__ __forceinline__ const float *seq_row(const float *base, const Run &r, int j, int C) {
-    const int s = __shfl_sync(kFull, r.seq, j);
+    const int s = __shfl_sync(kFull, r.seq, half() * L + j);
     return base ? base + static_cast<size_t>(s) * C : nullptr;
 }
 
@@ -353,7 +351,7 @@ __device__ __forceinline__ unsigned next_item(const RecParams &p, unsigned &deal
 // Shared memory of an item's joining: the runs, and the states that enter them.
 template <int W, bool kBack>
 struct Joins {
-    float4 run[W][32];
+    float4 run[W][32];    // the run of lane l's half of warp w
     float2 start[W][32];
     float2 sum[2][kBack ? W : 1][32];  // backward: the runs' sums of w, of this item and the one before
     int stop;
@@ -387,28 +385,34 @@ __device__ __forceinline__ float2 step_over(float4 r, float2 h) {
 
 // The joining warp's part of an item: publishes the chunk's (A, H), finds the state that enters the chunk,
 // publishes the one that leaves it, and hands out those that enter the runs.
-template <bool kEdge, bool kForward, int W, bool kAdjacent>
-__device__ __forceinline__ void join_runs(const RecParams &p, int chunk, bool needed, Published<kAdjacent> &front,
-                                          const float4 (*runs)[32], float2 (*start)[32], const Lane2<kAdjacent> &l) {
+template <bool kEdge, bool kForward, int W>
+__device__ __forceinline__ void join_runs(const RecParams &p, int chunk, bool needed, float2 h, Published &front,
+                                          const float4 (*runs)[32], float2 (*start)[32], const Lane2 &l) {
     constexpr int kStep = kForward ? 1 : -1;
     const int lane = threadIdx.x & 31;
     const int before = kForward ? chunk : p.chunks - 1 - chunk;
     const bool sends = (kForward ? chunk + 1 < p.chunks : chunk > 0) && !p.starve;
     const size_t at = static_cast<size_t>(chunk) * p.Cpad;
-    float4 all = make_float4(1.f, 0.f, 1.f, 0.f);
-    if (sends) {
+    // half the lanes join the first half of the runs, the others the second
+    const auto place = [&](int i) { return kForward ? half() * W + i : 2 * W - 1 - (half() * W + i); };
+    const auto run = [&](int i) { return runs[place(i) >> 1][(place(i) & 1) * 16 + lane16()]; };
+    const auto from_half = [&](const float4 &v, int h) {
+        return make_float4(__shfl_sync(kFull, v.x, h * 16 + lane16()), __shfl_sync(kFull, v.y, h * 16 + lane16()),
+                           __shfl_sync(kFull, v.z, h * 16 + lane16()), __shfl_sync(kFull, v.w, h * 16 + lane16()));
+    };
+    float4 mine = run(0);
 #pragma unroll
-        for (int i = 0; i < W; ++i) all = join<kEdge>(all, runs[kForward ? i : W - 1 - i][lane]);
-        if (!kEdge) {
-            all.x = fmaxf(all.x, kLeast);
-            all.z = fmaxf(all.z, kLeast);
-        }
-        if (needed) {
-            publish(p.aggregate + at + l.c0, all.x, all.y);
-            publish(p.aggregate + at + l.c1, all.z, all.w);
-        }
+    for (int i = 1; i < W; ++i) mine = join<kEdge>(mine, run(i));
+    const float4 first = from_half(mine, 0);
+    float4 all = join<kEdge>(first, from_half(mine, 1));
+    if (!kEdge) {
+        all.x = fmaxf(all.x, kLeast);
+        all.z = fmaxf(all.z, kLeast);
     }
-    float2 h = splat(0.f);
+    if (sends && needed && half() == 0) {
+        publish(p.aggregate + at + l.c0, all.x, all.y);
+        publish(p.aggregate + at + l.c1, all.z, all.w);
+    }
     if (needed) {
         uint64_t began = 0;
         for (unsigned i = 1; !front.state(h); ++i) {
@@ -424,15 +428,15 @@ __device__ __forceinline__ void join_runs(const RecParams &p, int chunk, bool ne
             front.read(p, chunk, before, kStep, l);
         }
     }
-    if (sends) {
+    if (sends && half() == 0) {
         publish(p.carry + at + l.c0, after(all.x, all.y, h.x));
         publish(p.carry + at + l.c1, after(all.z, all.w, h.y));
     }
+    if (half()) h = step_over<kEdge>(first, h);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-        const int w = kForward ? i : W - 1 - i;
-        start[w][lane] = h;
-        h = step_over<kEdge>(runs[w][lane], h);
+        start[place(i) >> 1][(place(i) & 1) * 16 + lane16()] = h;
+        h = step_over<kEdge>(run(i), h);
     }
 }
 
@@ -449,6 +453,7 @@ __device__ __forceinline__ bool forward_item(const RecParams &p, Rows &rows, con
 #pragma unroll
     for (int j = 0; j < L; ++j) {
         if (j == L / 2) halfway();
+        const float *from = kEdge ? seq_row<L>(p.state, run, j, p.C) : nullptr;
         if (kEdge && !(run.in >> j & 1u)) {
             A[j] = H[j] = splat(0.f);
             continue;
@@ -457,7 +462,7 @@ __device__ __forceinline__ bool forward_item(const RecParams &p, Rows &rows, con
         const float2 b = contribution(pm, sigmoid2(rows.get(kGateX, j)), rows.get(kX, j)), a = add1(pm, 1.f);
         if (kEdge && (run.start >> j & 1u)) {
             A[j] = splat(0.f);
-            H[j] = fma2(a, load_f32(seq_row(p.state, run, j, p.C), rows.l), b);
+            H[j] = fma2(a, load_f32(from, rows.l), b);
         } else {
             if (kEdge) A[j] = j ? product(A[j ? j - 1 : 0], no_cut(a)) : no_cut(a);
             else A[j] = j ? mul2(A[j ? j - 1 : 0], a) : a;
@@ -469,22 +474,24 @@ __device__ __forceinline__ bool forward_item(const RecParams &p, Rows &rows, con
     float2 y = h;
 #pragma unroll
     for (int j = 0; j < L; ++j) {
+        const float *to = kEdge ? seq_row<L>(p.final_state, run, j, p.C) : nullptr;
         if (kEdge && !(run.in >> j & 1u)) continue;
         if (j % kRecRun == 0 && p.saved) store2(p.saved + static_cast<size_t>(rows.saved + j / kRecRun) * p.Cpad, y, rows.l);
         y = kEdge ? make_float2(after(A[j].x, H[j].x, h.x), after(A[j].y, H[j].y, h.y)) : fma2(A[j], h, H[j]);
         rows.put(0, j, y);
         if (kEdge && (run.end >> j & 1u) && p.final_state)
-            store2(const_cast<float *>(seq_row(p.final_state, run, j, p.C)), y, rows.l);
+            store2(const_cast<float *>(to), y, rows.l);
     }
+    if (!kEdge && run.end && p.final_state) store2(p.final_state + static_cast<size_t>(run.seq) * p.C, y, rows.l);
     rows.done(1);
     return true;
 }
 
 // What a state leaves of an empty sequence: itself.
-template <int kWarps, bool kAdjacent>
-__device__ __forceinline__ void copy_empty(const Sequences &q, const float *from, float *to, int C, const Lane2<kAdjacent> &l) {
+template <int kWarps>
+__device__ __forceinline__ void copy_empty(const Sequences &q, const float *from, float *to, int C, const Lane2 &l) {
     if (!to) return;
-    for (int s = threadIdx.x >> 5; s < q.nseq; s += kWarps)
+    for (int s = threadIdx.x >> 4; s < q.nseq; s += 2 * kWarps)
         if (seq_begin(q, s + 1) <= seq_begin(q, s))
             store2(to + static_cast<size_t>(s) * C, load_f32(from ? from + static_cast<size_t>(s) * C : nullptr, l), l);
 }
@@ -501,17 +508,19 @@ __device__ __forceinline__ bool backward_item(const RecParams &p, Rows &rows, co
     constexpr int L = Rows::kRun;
     static_assert(L == kRecRun, "a saved state for each run");
     float2 h = splat(0.f);  // what enters the run
-    if (!kEdge || (run.in & 1u)) h = load2<float>(p.saved + static_cast<size_t>(rows.saved) * p.Cpad, rows.l);
+    if (!kEdge && run.start) h = load_f32(p.state ? p.state + static_cast<size_t>(run.seq) * p.C : nullptr, rows.l);
+    else if (!kEdge || (run.in & 1u)) h = load2<float>(p.saved + static_cast<size_t>(rows.saved) * p.Cpad, rows.l);
     const float2 rate = decay_rate(p, rows.l);
     float2 pm[L], ra[L], rx[L], before[L];  // a - 1, the gates, h[t-1]
 #pragma unroll
     for (int j = 0; j < L; ++j) {
         if (j == L / 2) halfway();
+        const float *from = kEdge ? seq_row<L>(p.state, run, j, p.C) : nullptr;
         if (kEdge && !(run.in >> j & 1u)) continue;
         ra[j] = sigmoid2(rows.get(kGateA, j));
         rx[j] = sigmoid2(rows.get(kGateX, j));
         pm[j] = exp2m1(mul2(rate, ra[j]));
-        if (kEdge && (run.start >> j & 1u)) h = load_f32(seq_row(p.state, run, j, p.C), rows.l);
+        if (kEdge && (run.start >> j & 1u)) h = load_f32(from, rows.l);
         before[j] = h;
         h = fma2(add1(pm[j], 1.f), h, contribution(pm[j], rx[j], rows.get(kX, j)));
     }
@@ -519,13 +528,14 @@ __device__ __forceinline__ bool backward_item(const RecParams &p, Rows &rows, co
     float2 g = splat(0.f), a = splat(0.f), B = splat(1.f);
 #pragma unroll
     for (int j = L - 1; j >= 0; --j) {
+        const float *behind = kEdge ? seq_row<L>(p.d_final, run, j, p.C) : nullptr;
         if (kEdge && !(run.in >> j & 1u)) {
             g = a = B = splat(0.f);
             continue;
         }
         const float2 dh = rows.get(kDy, j);
         if (kEdge && (run.end >> j & 1u)) {
-            g = add2(dh, load_f32(seq_row(p.d_final, run, j, p.C), rows.l));
+            g = add2(dh, load_f32(behind, rows.l));
             B = splat(0.f);
         } else {
             g = j < L - 1 ? fma2(a, g, dh) : dh;
@@ -541,12 +551,14 @@ __device__ __forceinline__ bool backward_item(const RecParams &p, Rows &rows, co
     g = a = splat(0.f);
 #pragma unroll
     for (int j = L - 1; j >= 0; --j) {
+        const float *behind = kEdge ? seq_row<L>(p.d_final, run, j, p.C) : nullptr;
+        const float *to = kEdge ? seq_row<L>(p.d_state, run, j, p.C) : nullptr;
         if (kEdge && !(run.in >> j & 1u)) {
             g = a = splat(0.f);
             continue;
         }
         const float2 dh = rows.get(kDy, j), x = rows.get(kX, j);
-        if (kEdge && (run.end >> j & 1u)) g = add2(dh, load_f32(seq_row(p.d_final, run, j, p.C), rows.l));
+        if (kEdge && (run.end >> j & 1u)) g = add2(dh, load_f32(behind, rows.l));
         else g = j < L - 1 ? fma2(a, g, dh) : add2(dh, G);
         a = add1(pm[j], 1.f);
         const float2 back = mul2(a, g), ga = mul2(ra[j], back), bx = mul2(rx[j], x);
@@ -564,7 +576,8 @@ __device__ __forceinline__ bool backward_item(const RecParams &p, Rows &rows, co
         rows.put(1, j, da);
         rows.put(2, j, dg);
         if (kEdge && (run.start >> j & 1u) && p.d_state)
-            store2(const_cast<float *>(seq_row(p.d_state, run, j, p.C)), back, rows.l);
+            store2(const_cast<float *>(to), back, rows.l);
+        if (!kEdge && j == 0 && run.start && p.d_state) store2(p.d_state + static_cast<size_t>(run.seq) * p.C, back, rows.l);
     }
     rows.done(3);
     s_sum[warp][threadIdx.x & 31] = sum;
@@ -584,12 +597,15 @@ __device__ __noinline__ bool work_item_edges(const RecParams &p, Rows rows, Run 
     return work_item<true, W, kBack>(p, rows, run, s, s_sum, warp, halfway);
 }
 
-// The chunk's sum of w, its warps' in order.
-template <int W, bool kAdjacent>
-__device__ __forceinline__ void store_sum(const RecParams &p, int chunk, const float2 (*s_sum)[32], const Lane2<kAdjacent> &l) {
+// The chunk's sum of w, its halves' and their warps' in order.
+template <int W>
+__device__ __forceinline__ void store_sum(const RecParams &p, int chunk, const float2 (*s_sum)[32], const Lane2 &l) {
     float2 sum = splat(0.f);
 #pragma unroll
     for (int w = 0; w < W; ++w) sum = add2(sum, s_sum[w][threadIdx.x & 31]);
+    sum.x += __shfl_xor_sync(kFull, sum.x, 16);
+    sum.y += __shfl_xor_sync(kFull, sum.y, 16);
+    if (half()) return;
     float *out = p.decay_partial + static_cast<size_t>(chunk) * p.Cpad;
     out[l.c0] = sum.x;
     out[l.c1] = sum.y;
@@ -621,12 +637,15 @@ struct Item {
     int chunk;  // -1: no more items
     int tile, row0;
     int saved;  // saved_place of its first run
-    int flags;  // kEdges: has edges; kFirst: the first of all
+    int flags;
+    int seq;    // its first row's sequence
 };
-enum : int { kEdges = 1, kFirst = 2 };
+// An item is the first of all; a sequence begins or ends inside it, or rows of it belong to none, so that its rows are looked
+// at one by one; else its rows are the first, the last of their sequence.
+enum : int { kFirst = 1, kEdges = 2, kStarts = 4, kEnds = 8 };
 
 __device__ __forceinline__ Item item_of(const RecParams &p, unsigned item, int chunk_rows, bool back) {
-    if (item >= static_cast<unsigned>(p.chunks) * p.tiles) return Item{-1, 0, 0, 0, 0};
+    if (item >= static_cast<unsigned>(p.chunks) * p.tiles) return Item{-1, 0, 0, 0, 0, 0};
     const int turn = item / p.tiles, tile = item - turn * p.tiles;
     int chunk = back ? p.chunks - 1 - turn : turn;
     if (p.per_seq) {
@@ -634,68 +653,122 @@ __device__ __forceinline__ Item item_of(const RecParams &p, unsigned item, int c
         chunk = s * p.per_seq + (back ? p.per_seq - 1 - k : k);
     }
     const int row0 = chunk_row(p, chunk, chunk_rows);
-    return Item{chunk, tile, row0, saved_place(p, chunk, row0), (has_edges(p.seq, row0, chunk_rows) ? kEdges : 0) | (item == 0 ? kFirst : 0)};
+    const int seq = seq_of(p.seq, row0), begin = seq < 0 ? 0 : seq_begin(p.seq, seq), end = seq < 0 ? 0 : seq_begin(p.seq, seq + 1);
+    int flags = item == 0 ? kFirst : 0;
+    if (begin > row0 || end < row0 + chunk_rows) flags |= kEdges;
+    else flags |= (begin == row0 ? kStarts : 0) | (end == row0 + chunk_rows ? kEnds : 0);
+    return Item{chunk, tile, row0, saved_place(p, chunk, row0), flags, seq};
+}
+
+// Which of a warp's rows belong to a sequence, from its two runs.
+template <int L>
+__device__ __forceinline__ unsigned present_rows(const Run &run) {
+    return __shfl_sync(kFull, run.in, 0) | __shfl_sync(kFull, run.in, 16) << L;
+}
+
+// A run of a chunk of one sequence.
+template <int W>
+__device__ __forceinline__ Run whole_run(const Item &item) {
+    const int place = threadIdx.x >> 4;
+    return Run{~0u, (item.flags & kStarts) && place == 0, (item.flags & kEnds) && place == 2 * W - 1, item.seq};
 }
 
 // The joining warp's work on an item: first, while the runs are still at work, it looks for what is in front.
-template <int W, int L, bool kBack, bool kAdjacent>
+template <int W, int L, bool kBack>
 struct Joining {
-    Published<kAdjacent> front;
+    Published front;
     bool needed;  // whether the rows in front of the chunk (against the order of time: behind it) reach into it
-    __device__ __forceinline__ void look(const RecParams &p, const Item &item, const Lane2<kAdjacent> &l) {
+    float2 h;     // what enters the chunk where none do
+    __device__ __forceinline__ void look(const RecParams &p, const Item &item, const Lane2 &l) {
         const int chunk = item.chunk;
         needed = kBack ? chunk + 1 < p.chunks : chunk > 0;
-        if (item.flags & kEdges) {
+        h = splat(0.f);
+        if (item.flags & (kBack ? kEnds : kStarts)) {
+            const float *from = kBack ? p.d_final : p.state;
+            needed = false;
+            h = load_f32(from ? from + static_cast<size_t>(item.seq) * p.C : nullptr, l);
+        } else if (item.flags & kEdges) {
             if (p.per_seq) {
                 needed = (kBack ? chunk + 1 : chunk) % p.per_seq != 0;
             } else if (needed) {
-                const int row0 = item.row0, row1 = row0 + W * L, s = seq_of(p.seq, kBack ? row1 - 1 : row0);
+                const int row0 = item.row0, row1 = row0 + 2 * W * L, s = seq_of(p.seq, kBack ? row1 - 1 : row0);
                 needed = s >= 0 && (kBack ? row1 < seq_begin(p.seq, s + 1) : seq_begin(p.seq, s) < row0 && row0 < seq_begin(p.seq, s + 1));
             }
         }
         if (needed) front.read(p, chunk, kBack ? p.chunks - 1 - chunk : chunk, kBack ? -1 : 1, l);
     }
     __device__ __forceinline__ void join(const RecParams &p, const Item &item, const float4 (*runs)[32], float2 (*start)[32],
-                                         const Lane2<kAdjacent> &l) {
-        if (item.flags & kEdges) join_runs<true, !kBack, W>(p, item.chunk, needed, front, runs, start, l);
-        else join_runs<false, !kBack, W>(p, item.chunk, needed, front, runs, start, l);
+                                         const Lane2 &l) {
+        if (item.flags & kEdges) join_runs<true, !kBack, W>(p, item.chunk, needed, h, front, runs, start, l);
+        else join_runs<false, !kBack, W>(p, item.chunk, needed, h, front, runs, start, l);
     }
 };
 
-// Items element by element, for tensors that TMA does not take.
+// Items whose rows the warps copy themselves, for tensors that TMA does not take: the next item's while one is at work.
 template <typename T, int W, int L, bool kBack>
 __global__ void __launch_bounds__((W + 1) * 32, 2) rec_plain_kernel(const __grid_constant__ RecParams p) {
+    using Tile = TileRun<T, 2 * W * L, L, false>;
+    constexpr int kIn = kBack ? 4 : 3, kAll = (W + 1) * 32;
+    extern __shared__ __align__(128) uint8_t s_tiles[];
     __shared__ Joins<W, kBack> s;
-    __shared__ Item s_item;
+    __shared__ Item s_item[2];
     const int warp = threadIdx.x >> 5;
     unsigned dealt = blockIdx.x;
-    if (threadIdx.x == 0) s.stop = 0;
-    for (;;) {
-        __syncthreads();
-        if (threadIdx.x == 0) s_item = item_of(p, next_item(p, dealt), W * L, kBack);
-        __syncthreads();
-        const Item item = s_item;
+    const auto tile_of = [&](const Item &item, int stage) {
+        return Tile(p, nullptr, s_tiles + stage * kIn * Tile::kTensor, warp, item.tile, item.row0 + warp * 2 * L,
+                    item.saved + (warp * 2 + half()) * (L / kRecRun));
+    };
+    Item ahead{-1, 0, 0, 0, 0, 0};  // one thread's: the next item, taken while nothing waits for it
+    const auto take = [&] {
+        if (threadIdx.x == W * 32) ahead = item_of(p, next_item(p, dealt), 2 * W * L, kBack);
+    };
+    take();
+    if (threadIdx.x == W * 32) {
+        s.stop = 0;
+        s_item[0] = ahead;
+    }
+    take();
+    __syncthreads();
+    if (warp < W && s_item[0].chunk >= 0) tile_of(s_item[0], 0).fetch(kIn);
+    for (unsigned n = 0;; ++n) {
+        const Item item = s_item[n & 1];
         if (item.chunk < 0) break;
-        const int row0 = item.row0 + warp * L;
-        GlobalRun<T, L> rows(p, item.tile, row0, item.saved + warp * L / kRecRun);
+        if (threadIdx.x == W * 32) s_item[~n & 1] = ahead;
+        __syncthreads();
         if (item.flags & kFirst) check_offsets(p.seq, p.status);
         if (item.chunk == 0)
-            copy_empty<W + 1>(p.seq, kBack ? p.d_final : p.state, kBack ? p.d_state : p.final_state, p.C, rows.l);
+            copy_empty<W + 1>(p.seq, kBack ? p.d_final : p.state, kBack ? p.d_state : p.final_state, p.C, Lane2(item.tile, p.C));
         auto nothing = [] {};
         if (warp == W) {
-            Joining<W, L, kBack, false> joining;
-            joining.look(p, item, rows.l);
-            ptx::named_barrier(kRunsIn, (W + 1) * 32);
-            joining.join(p, item, s.run, s.start, rows.l);
-            named_barrier_arrive(kStartsIn, (W + 1) * 32);
-        } else if (item.flags & kEdges) {
-            work_item_edges<W, kBack>(p, rows, run_of<L>(p.seq, row0, chunk_limit(p, item.chunk)), s, s.sum[0], warp, nothing);
+            const Lane2 l(item.tile, p.C);
+            Joining<W, L, kBack> joining;
+            joining.look(p, item, l);
+            ptx::named_barrier(kRunsIn, kAll);
+            joining.join(p, item, s.run, s.start, l);
+            __syncwarp();
+            named_barrier_arrive(kStartsIn, kAll);
+            take();
         } else {
-            work_item<false, W, kBack>(p, rows, Run{~0u, 0u, 0u, 0}, s, s.sum[0], warp, nothing);
+            const Item next = s_item[~n & 1];
+            if (next.chunk >= 0) {
+                tile_of(next, ~n & 1).fetch(kIn);
+                cp_async_wait<1>();
+            } else {
+                cp_async_wait<0>();
+            }
+            __syncwarp();
+            Tile rows = tile_of(item, n & 1);
+            if (item.flags & kEdges) {
+                const Run run = run_of<L>(p.seq, rows.row0, chunk_limit(p, item.chunk));
+                rows.present = present_rows<L>(run);
+                work_item_edges<W, kBack>(p, rows, run, s, s.sum[0], warp, nothing);
+            } else {
+                work_item<false, W, kBack>(p, rows, whole_run<W>(item), s, s.sum[0], warp, nothing);
+            }
         }
         if constexpr (kBack) {
             __syncthreads();
-            if (warp == W) store_sum<W>(p, item.chunk, s.sum[0], rows.l);
+            if (warp == W) store_sum<W>(p, item.chunk, s.sum[0], Lane2(item.tile, p.C));
         }
     }
 }
@@ -705,7 +778,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 2) rec_plain_kernel(const __grid
 template <typename T, int W, int L, int S, bool kBack, int kBlocks>
 __global__ void __launch_bounds__((W + 1) * 32, kBlocks) rec_tile_kernel(const __grid_constant__ RecTiles q) {
     static_assert(S >= 2, "one item at work, one on its way");
-    using Tile = TileRun<T, W * L, L>;
+    using Tile = TileRun<T, 2 * W * L, L, true>;
     constexpr int kIn = kBack ? 4 : 3, kAll = (W + 1) * 32;
     constexpr int kStage = kIn * Tile::kTensor;
     extern __shared__ __align__(128) uint8_t s_tiles[];
@@ -725,9 +798,9 @@ __global__ void __launch_bounds__((W + 1) * 32, kBlocks) rec_tile_kernel(const _
     const ptx::Watchdog wd{&s_abort, p.status, static_cast<uint64_t>(p.timeout_ns)};
     if (warp == W) {
         unsigned dealt = blockIdx.x;
-        Item ahead{-1, 0, 0, 0, 0};  // lane 0: the item to be loaded next, taken while nothing waits for it
+        Item ahead{-1, 0, 0, 0, 0, 0};  // lane 0: the item to be loaded next, taken while nothing waits for it
         auto take = [&] {
-            if (lane == 0) ahead = item_of(p, next_item(p, dealt), W * L, kBack);
+            if (lane == 0) ahead = item_of(p, next_item(p, dealt), 2 * W * L, kBack);
         };
         auto issue = [&](int stage) {  // its loads
             if (lane == 0) {
@@ -756,11 +829,11 @@ __global__ void __launch_bounds__((W + 1) * 32, kBlocks) rec_tile_kernel(const _
         for (;; ++n) {
             const Item item = s_item[n % S];
             if (item.chunk < 0) break;
-            const Lane2<true> l(item.tile, p.C);
+            const Lane2 l(item.tile, p.C);
             if (item.flags & kFirst) check_offsets(p.seq, p.status, lane, 32);
             ptx::mbar_wait(&s_free, n & 1u, wd, kDevTimeoutEmpty);
             if (n > 0) issue((n - 1) % S);
-            Joining<W, L, kBack, true> joining;
+            Joining<W, L, kBack> joining;
             joining.look(p, item, l);
             ptx::named_barrier(kRunsIn, kAll);
             stop = *static_cast<volatile int *>(&s_abort) != 0;
@@ -770,7 +843,7 @@ __global__ void __launch_bounds__((W + 1) * 32, kBlocks) rec_tile_kernel(const _
             named_barrier_arrive(kStartsIn, kAll);
             if (stop) break;
             if constexpr (kBack) {
-                if (one.x >= 0) store_sum<W>(p, one.x, s.sum[~n & 1], Lane2<true>(one.y, p.C));
+                if (one.x >= 0) store_sum<W>(p, one.x, s.sum[~n & 1], Lane2(one.y, p.C));
             }
             if (n > 0) take();
             one = make_int2(item.chunk, item.tile);
@@ -783,7 +856,7 @@ __global__ void __launch_bounds__((W + 1) * 32, kBlocks) rec_tile_kernel(const _
             }
         } else if constexpr (kBack) {
             ptx::named_barrier(kEnd, kAll);
-            if (one.x >= 0) store_sum<W>(p, one.x, s.sum[~n & 1], Lane2<true>(one.y, p.C));
+            if (one.x >= 0) store_sum<W>(p, one.x, s.sum[~n & 1], Lane2(one.y, p.C));
         }
         return;
     }
@@ -802,10 +875,10 @@ __global__ void __launch_bounds__((W + 1) * 32, kBlocks) rec_tile_kernel(const _
         const Item item = s_item[stage];
         if (item.chunk < 0) break;
         const bool edges = item.flags & kEdges;
-        const int row0 = item.row0 + warp * L;
-        const Run run = edges ? run_of<L>(p.seq, row0, chunk_limit(p, item.chunk)) : Run{~0u, 0u, 0u, 0};
-        Tile rows(p, q.out, s_tiles + stage * kStage, item.tile, row0, item.saved + warp * L / kRecRun, warp,
-                  (run.in & ((1u << L) - 1u)) == (1u << L) - 1u);
+        const int row0 = item.row0 + warp * 2 * L;
+        const Run run = edges ? run_of<L>(p.seq, row0, chunk_limit(p, item.chunk)) : whole_run<W>(item);
+        Tile rows(p, q.out, s_tiles + stage * kStage, warp, item.tile, row0, item.saved + (warp * 2 + half()) * (L / kRecRun));
+        if (edges) rows.present = present_rows<L>(run);
         if (item.chunk == 0)
             copy_empty<W>(p.seq, kBack ? p.d_final : p.state, kBack ? p.d_state : p.final_state, p.C, rows.l);
         fine = edges ? work_item_edges<W, kBack>(p, rows, run, s, s.sum[n & 1], warp, halfway)
@@ -852,11 +925,12 @@ __global__ void __launch_bounds__(256) rec_init_kernel(uint4 *words, size_t n, c
     for (size_t c = i0; c < static_cast<size_t>(C); c += step) rates[c] = decay_rate(decay[c], kappa);
 }
 
-// One token: a block takes 256 channels of one row.
+// One token: a block takes kRecStepTile channels of one row.
 template <typename T>
-__global__ void __launch_bounds__(128) rec_step_kernel(const __grid_constant__ RecStepParams p) {
+__global__ void __launch_bounds__(kRecStepTile / 2) rec_step_kernel(const __grid_constant__ RecStepParams p) {
     const int b = blockIdx.x / p.tiles;
-    const Lane2<false> l(blockIdx.x % p.tiles * 4 + (threadIdx.x >> 5), p.C);
+    const int c = blockIdx.x % p.tiles * kRecStepTile + threadIdx.x;
+    const Lane2 l(c, c + kRecStepTile / 2, p.C);
     const int slot = p.slots ? p.slots[b] : b;
     const float2 x = load2<T>(static_cast<const T *>(p.x) + static_cast<size_t>(b) * p.ldx, l);
     const float2 ga = load2<T>(static_cast<const T *>(p.ga) + static_cast<size_t>(b) * p.lda, l);
@@ -876,7 +950,7 @@ __global__ void __launch_bounds__(128) rec_step_kernel(const __grid_constant__ R
     store2<float>(state, h, l);
 }
 
-// Resident blocks of a kernel, looked up once per device (and its shared memory allowed).
+// Resident blocks of a kernel, looked up once per device, when its shared memory is allowed.
 template <typename K>
 cudaError_t resident_blocks(K kernel, int threads, size_t smem, std::atomic<int> *known, int *blocks) {
     int dev = 0;
@@ -884,10 +958,8 @@ cudaError_t resident_blocks(K kernel, int threads, size_t smem, std::atomic<int>
     if (e != cudaSuccess) return e;
     *blocks = dev < kMaxKnown ? known[dev].load(std::memory_order_relaxed) : 0;
     if (*blocks) return cudaSuccess;
-    if (smem) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
     int per_sm = 0, sms = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -905,19 +977,20 @@ int grid_of(const RecParams &p, int blocks) {
 template <typename T, bool kBack>
 cudaError_t launch_plain(const RecParams &p, cudaStream_t s) {
     constexpr RecShape k = rec_shape(sizeof(T), kBack);
+    constexpr size_t smem = 2 * static_cast<size_t>(kBack ? 4 : 3) * TileRun<T, k.rows(), k.run, false>::kTensor;
     static std::atomic<int> known[kMaxKnown];
     int blocks = 0;
     const auto kernel = rec_plain_kernel<T, k.warps, k.run, kBack>;
-    const cudaError_t e = resident_blocks(kernel, (k.warps + 1) * 32, 0, known, &blocks);
+    const cudaError_t e = resident_blocks(kernel, (k.warps + 1) * 32, smem, known, &blocks);
     if (e != cudaSuccess) return e;
-    kernel<<<grid_of(p, blocks), (k.warps + 1) * 32, 0, s>>>(p);
+    kernel<<<grid_of(p, blocks), (k.warps + 1) * 32, smem, s>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T, bool kBack>
 cudaError_t launch_tiles(const RecTiles &q, cudaStream_t s) {
     constexpr RecShape k = rec_shape(sizeof(T), kBack);
-    constexpr size_t smem = static_cast<size_t>(k.stages) * (kBack ? 4 : 3) * TileRun<T, k.warps * k.run, k.run>::kTensor;
+    constexpr size_t smem = static_cast<size_t>(k.stages) * (kBack ? 4 : 3) * TileRun<T, k.rows(), k.run, true>::kTensor;
     static std::atomic<int> known[kMaxKnown];
     int blocks = 0;
     const auto kernel = rec_tile_kernel<T, k.warps, k.run, k.stages, kBack, k.blocks>;
@@ -954,8 +1027,8 @@ cudaError_t launch_rec_decay(const float *partial, const float *decay, float kap
 }
 
 cudaError_t launch_rec_step(const RecStepParams &p, bool f32, cudaStream_t s) {
-    if (f32) rec_step_kernel<float><<<p.B * p.tiles, 128, 0, s>>>(p);
-    else rec_step_kernel<__nv_bfloat16><<<p.B * p.tiles, 128, 0, s>>>(p);
+    if (f32) rec_step_kernel<float><<<p.B * p.tiles, kRecStepTile / 2, 0, s>>>(p);
+    else rec_step_kernel<__nv_bfloat16><<<p.B * p.tiles, kRecStepTile / 2, 0, s>>>(p);
     return cudaGetLastError();
 }
 

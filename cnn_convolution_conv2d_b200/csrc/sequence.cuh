@@ -84,7 +84,7 @@ struct RecParams {
 // The recurrence in tiles that travel by TMA.
 struct RecTiles {
     CUtensorMap in[4];     // x, gate_a, gate_x, dy as {C, rows}: boxes of kRecTile x a chunk's rows
-    CUtensorMap out[3];    // y, or dx, d_gate_a, d_gate_x: boxes of kRecTile x a run's rows
+    CUtensorMap out[3];    // y, or dx, d_gate_a, d_gate_x: boxes of kRecTile x the rows of a warp's two runs
     RecParams p;
 };
 
@@ -103,13 +103,15 @@ struct RecStepParams {
 constexpr int kConvWarps = 4;     // warps of a conv1d block, one strip of rows each
 constexpr int kConvBlocks = 6, kConvBlocksBack = 4;  // blocks an SM
 constexpr int kConvBatch = 16;    // bytes of one channel's rows in a batch: 8 rows in bf16, 4 in fp32
-constexpr int kRecTile = 64;      // channels of a work item of the recurrence
+constexpr int kRecTile = 32;      // channels of a work item of the recurrence
+constexpr int kRecStepTile = 256; // channels of a block of its step
 constexpr int kRecRun = 8;        // rows of one saved state
 
-// How a kernel of the recurrence is laid out: working warps, rows that one scans, stages of shared memory, blocks an SM.
+// How a kernel of the recurrence is laid out: working warps, rows that half of one scans, stages of shared memory,
+// blocks an SM.
 struct RecShape {
     int warps, run, stages, blocks;
-    constexpr int rows() const { return warps * run; }
+    constexpr int rows() const { return 2 * warps * run; }
 };
 constexpr RecShape rec_shape(int elt, bool back) {
     return back ? (elt == 2 ? RecShape{7, 8, 2, 2} : RecShape{6, 8, 2, 2}) : (elt == 2 ? RecShape{8, 16, 2, 2} : RecShape{8, 8, 2, 2});

@@ -104,7 +104,7 @@ bool tile_map(const void *ptr, long long stride, long long rows, int C, int elt,
     return abi_tensor_map_2d(map, ptr, elt, C, rows, bytes, box_cols, box_rows) == CONV_OK;
 }
 
-// The recurrence's scratch: [counter][aggregates][carries][decay rates][decay sums], each at a multiple of 256 bytes.
+// The recurrence's scratch: [counter][aggregates][carries][decay rates][decay sums], each at a multiple of 128 bytes.
 struct RecLayout {
     int chunks, per_seq, tiles, Cpad, chunk_rows;
     size_t aggregate, carry, rates, decay, forward_total, backward_total;
@@ -145,7 +145,7 @@ int rec_layout(int nseq, int T, long long rows, int C, conv_dtype_t dtype, bool 
     r->tiles = static_cast<int>(tiles);
     r->chunk_rows = static_cast<int>(chunk_rows);
     r->Cpad = r->tiles * kRecTile;
-    const size_t each = static_cast<size_t>(chunks) * r->Cpad * 4;  // a multiple of 256
+    const size_t each = static_cast<size_t>(chunks) * r->Cpad * 4;  // a multiple of 128
     const bool joins = chunks > 1;
     r->aggregate = joins ? 256 : 0;
     r->carry = r->aggregate + (joins ? 2 * each : 0);
@@ -176,15 +176,15 @@ int rec_begin(RecParams *p, const RecLayout &r, void *workspace, cudaStream_t st
 int run_rec(const RecParams &p, const RecLayout &r, int elt, bool back, cudaStream_t s) {
     RecTiles q{};
     const long long rows = p.seq.rows;
-    const int run = rec_shape(elt, back).run, chunk = r.chunk_rows;
+    const int runs = 2 * rec_shape(elt, back).run, chunk = r.chunk_rows;
     bool tiles = tile_map(p.x, p.ldx, rows, p.C, elt, kRecTile, chunk, &q.in[0]) &&
                  tile_map(p.ga, p.lda, rows, p.C, elt, kRecTile, chunk, &q.in[1]) &&
                  tile_map(p.gx, p.ldg, rows, p.C, elt, kRecTile, chunk, &q.in[2]) &&
-                 tile_map(p.y, p.ldy, rows, p.C, elt, kRecTile, run, &q.out[0]);
+                 tile_map(p.y, p.ldy, rows, p.C, elt, kRecTile, runs, &q.out[0]);
     if (back)
         tiles = tiles && tile_map(p.dy, p.lddy, rows, p.C, elt, kRecTile, chunk, &q.in[3]) &&
-                tile_map(p.dga, p.ld_da, rows, p.C, elt, kRecTile, run, &q.out[1]) &&
-                tile_map(p.dgx, p.ld_dg, rows, p.C, elt, kRecTile, run, &q.out[2]);
+                tile_map(p.dga, p.ld_da, rows, p.C, elt, kRecTile, runs, &q.out[1]) &&
+                tile_map(p.dgx, p.ld_dg, rows, p.C, elt, kRecTile, runs, &q.out[2]);
     const char *what = back ? "recurrence gradient" : "recurrence";
     if (!tiles) return abi_launch(launch_rec_plain(p, elt == 4, back, s), what);
     q.p = p;
@@ -463,7 +463,7 @@ int gated_recurrence_step(const void *x, const void *gate_a, const void *gate_x,
     p.slots = slots;
     p.ldx = x_stride; p.lda = gate_a_stride; p.ldg = gate_x_stride; p.ldy = y_stride;
     p.B = B; p.C = C; p.pool = pool; p.status = dev.status;
-    p.tiles = static_cast<int>(ceil_div(C, 4 * kRecTile));
+    p.tiles = static_cast<int>(ceil_div(C, kRecStepTile));
     if (static_cast<long long>(p.tiles) * B > kMaxBlocks)
         return abi_fail(CONV_ERR_UNSUPPORTED, "too many rows and channels for one launch");
     RETURN_IF(abi_launch(launch_rec_step(p, elt == 4, reinterpret_cast<cudaStream_t>(stream)), "recurrence step"));
