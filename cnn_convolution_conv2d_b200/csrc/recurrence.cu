@@ -303,6 +303,18 @@ struct Published {
     }
 };
 
+// An item.
+struct Item {
+    int chunk;  // -1: no more items
+    int tile, row0;
+    int saved;  // saved_place of its first run
+    int flags;
+    int seq, last;  // the sequences of its first and its last row
+};
+// An item is the first of all; a sequence begins or ends inside it, or rows of it belong to none; else its rows are the
+// first, the last of their sequence; the rows in front of it (against the order of time: behind it) reach into it.
+enum : int { kFirst = 1, kEdges = 2, kStarts = 4, kEnds = 8, kNeedsFront = 16 };
+
 // What the rows of a half warp's run are, a bit each; `seq` of lane j is the sequence of the warp's row j.  In a chunk
 // of one sequence: whether the run begins or ends it, and the sequence.
 struct Run {
@@ -310,13 +322,13 @@ struct Run {
     int seq;
 };
 template <int L>
-__device__ __forceinline__ Run run_of(const Sequences &q, int row0, int limit) {
+__device__ __forceinline__ Run run_of(const Sequences &q, const Item &item, int row0, int limit) {
     const int lane = threadIdx.x & 31, row = row0 + lane;
     Run r;
     r.seq = 0;
     bool in = false, start = false, end = false;
     if (lane < 2 * L && row < limit) {
-        const int s = seq_of(q, row);
+        const int s = seq_of(q, row, item.seq, item.last);
         if (s >= 0) {
             const int b = seq_begin(q, s), e = seq_begin(q, s + 1);
             in = row < e;
@@ -447,10 +459,10 @@ __device__ __forceinline__ void join_runs(const RecParams &p, int chunk, bool ne
 template <bool kEdge, int W, typename Rows, typename Halfway>
 __device__ __forceinline__ bool forward_item(const RecParams &p, Rows &rows, const Run &run, Joins<W, false> &s, int warp,
                                              Halfway halfway) {
-    constexpr int L = Rows::kRun;
+    constexpr int L = Rows::kRun, kUnroll = kEdge ? 1 : L;
     float2 A[L], H[L];
     const float2 rate = decay_rate(p, rows.l);
-#pragma unroll
+#pragma unroll kUnroll
     for (int j = 0; j < L; ++j) {
         if (j == L / 2) halfway();
         const float *from = kEdge ? seq_row<L>(p.state, run, j, p.C) : nullptr;
@@ -469,10 +481,11 @@ __device__ __forceinline__ bool forward_item(const RecParams &p, Rows &rows, con
             H[j] = j ? fma2(a, H[j ? j - 1 : 0], b) : b;
         }
     }
-    if (!exchange(s, make_float4(A[L - 1].x, H[L - 1].x, A[L - 1].y, H[L - 1].y), warp)) return false;
+    const float2 all = kEdge ? A[L - 1] : no_cut(A[L - 1]);
+    if (!exchange(s, make_float4(all.x, H[L - 1].x, all.y, H[L - 1].y), warp)) return false;
     const float2 h = s.start[warp][threadIdx.x & 31];
     float2 y = h;
-#pragma unroll
+#pragma unroll kUnroll
     for (int j = 0; j < L; ++j) {
         const float *to = kEdge ? seq_row<L>(p.final_state, run, j, p.C) : nullptr;
         if (kEdge && !(run.in >> j & 1u)) continue;
@@ -505,14 +518,14 @@ __device__ __forceinline__ void copy_empty(const Sequences &q, const float *from
 template <bool kEdge, int W, typename Rows, typename Halfway>
 __device__ __forceinline__ bool backward_item(const RecParams &p, Rows &rows, const Run &run, Joins<W, true> &s,
                                               float2 (*s_sum)[32], int warp, Halfway halfway) {
-    constexpr int L = Rows::kRun;
+    constexpr int L = Rows::kRun, kUnroll = kEdge ? 1 : L;
     static_assert(L == kRecRun, "a saved state for each run");
     float2 h = splat(0.f);  // what enters the run
     if (!kEdge && run.start) h = load_f32(p.state ? p.state + static_cast<size_t>(run.seq) * p.C : nullptr, rows.l);
     else if (!kEdge || (run.in & 1u)) h = load2<float>(p.saved + static_cast<size_t>(rows.saved) * p.Cpad, rows.l);
     const float2 rate = decay_rate(p, rows.l);
     float2 pm[L], ra[L], rx[L], before[L];  // a - 1, the gates, h[t-1]
-#pragma unroll
+#pragma unroll kUnroll
     for (int j = 0; j < L; ++j) {
         if (j == L / 2) halfway();
         const float *from = kEdge ? seq_row<L>(p.state, run, j, p.C) : nullptr;
@@ -526,7 +539,7 @@ __device__ __forceinline__ bool backward_item(const RecParams &p, Rows &rows, co
     }
     // g from zero behind the run, the a of the row after, and the product of all a's so far
     float2 g = splat(0.f), a = splat(0.f), B = splat(1.f);
-#pragma unroll
+#pragma unroll kUnroll
     for (int j = L - 1; j >= 0; --j) {
         const float *behind = kEdge ? seq_row<L>(p.d_final, run, j, p.C) : nullptr;
         if (kEdge && !(run.in >> j & 1u)) {
@@ -544,12 +557,13 @@ __device__ __forceinline__ bool backward_item(const RecParams &p, Rows &rows, co
         B = kEdge ? product(B, no_cut(a)) : mul2(B, a);
     }
     const float2 S = mul2(a, g);
+    if (!kEdge) B = no_cut(B);
     if (!exchange(s, make_float4(B.x, S.x, B.y, S.y), warp)) return false;
     const float2 G = s.start[warp][threadIdx.x & 31];
     const float2 natural = mul2(decay_rate(p, rows.l), splat(1.f / kLog2e));
     float2 sum = splat(0.f);
     g = a = splat(0.f);
-#pragma unroll
+#pragma unroll kUnroll
     for (int j = L - 1; j >= 0; --j) {
         const float *behind = kEdge ? seq_row<L>(p.d_final, run, j, p.C) : nullptr;
         const float *to = kEdge ? seq_row<L>(p.d_state, run, j, p.C) : nullptr;
@@ -590,7 +604,8 @@ __device__ __forceinline__ bool work_item(const RecParams &p, Rows &rows, const 
     if constexpr (kBack) return backward_item<kEdge, W>(p, rows, run, s, s_sum, warp, halfway);
     else return forward_item<kEdge, W>(p, rows, run, s, warp, halfway);
 }
-// The form for chunks with edges, as a call: inlined, it would take registers from the other.
+// The form for rows with edges, as a call (inlined, it would take registers from the other) and in loops: unrolled, the
+// instructions of both forms together did not stay in the cache, and a packed batch took twice the time.
 template <int W, bool kBack, typename Rows, typename Halfway>
 __device__ __noinline__ bool work_item_edges(const RecParams &p, Rows rows, Run run, Joins<W, kBack> &s, float2 (*s_sum)[32],
                                              int warp, Halfway halfway) {
@@ -632,20 +647,8 @@ __device__ __forceinline__ int saved_place(const RecParams &p, int chunk, int ro
     return s * ((p.seq.T + kRecRun - 1) / kRecRun) + (row0 - s * p.seq.T) / kRecRun;
 }
 
-// An item.
-struct Item {
-    int chunk;  // -1: no more items
-    int tile, row0;
-    int saved;  // saved_place of its first run
-    int flags;
-    int seq;    // its first row's sequence
-};
-// An item is the first of all; a sequence begins or ends inside it, or rows of it belong to none, so that its rows are looked
-// at one by one; else its rows are the first, the last of their sequence.
-enum : int { kFirst = 1, kEdges = 2, kStarts = 4, kEnds = 8 };
-
 __device__ __forceinline__ Item item_of(const RecParams &p, unsigned item, int chunk_rows, bool back) {
-    if (item >= static_cast<unsigned>(p.chunks) * p.tiles) return Item{-1, 0, 0, 0, 0, 0};
+    if (item >= static_cast<unsigned>(p.chunks) * p.tiles) return Item{-1, 0, 0, 0, 0, 0, 0};
     const int turn = item / p.tiles, tile = item - turn * p.tiles;
     int chunk = back ? p.chunks - 1 - turn : turn;
     if (p.per_seq) {
@@ -655,15 +658,33 @@ __device__ __forceinline__ Item item_of(const RecParams &p, unsigned item, int c
     const int row0 = chunk_row(p, chunk, chunk_rows);
     const int seq = seq_of(p.seq, row0), begin = seq < 0 ? 0 : seq_begin(p.seq, seq), end = seq < 0 ? 0 : seq_begin(p.seq, seq + 1);
     int flags = item == 0 ? kFirst : 0;
-    if (begin > row0 || end < row0 + chunk_rows) flags |= kEdges;
-    else flags |= (begin == row0 ? kStarts : 0) | (end == row0 + chunk_rows ? kEnds : 0);
-    return Item{chunk, tile, row0, saved_place(p, chunk, row0), flags, seq};
+    const int row1 = row0 + chunk_rows;
+    int last = seq;
+    bool front = back ? chunk + 1 < p.chunks : chunk > 0;
+    if (begin > row0 || end < row1) {
+        flags |= kEdges;
+        last = seq_of(p.seq, row1 - 1);
+        if (p.per_seq) front = (back ? chunk + 1 : chunk) % p.per_seq != 0;
+        else if (back) front = front && last >= 0 && row1 < seq_begin(p.seq, last + 1);
+        else front = front && begin < row0 && row0 < end;
+    } else {
+        flags |= (begin == row0 ? kStarts : 0) | (end == row1 ? kEnds : 0);
+        front = front && (back ? end != row1 : begin != row0);
+    }
+    if (front) flags |= kNeedsFront;
+    return Item{chunk, tile, row0, saved_place(p, chunk, row0), flags, seq, last};
 }
 
 // Which of a warp's rows belong to a sequence, from its two runs.
 template <int L>
 __device__ __forceinline__ unsigned present_rows(const Run &run) {
     return __shfl_sync(kFull, run.in, 0) | __shfl_sync(kFull, run.in, 16) << L;
+}
+
+// Whether a sequence begins or ends in a warp's rows, or some belong to none: then they are looked at one by one.
+template <int L>
+__device__ __forceinline__ bool row_by_row(const Item &item, const Run &run) {
+    return item.flags & kEdges && __any_sync(kFull, run.in != (1u << L) - 1u || run.start || run.end);
 }
 
 // A run of a chunk of one sequence.
@@ -677,30 +698,20 @@ __device__ __forceinline__ Run whole_run(const Item &item) {
 template <int W, int L, bool kBack>
 struct Joining {
     Published front;
-    bool needed;  // whether the rows in front of the chunk (against the order of time: behind it) reach into it
-    float2 h;     // what enters the chunk where none do
+    float2 h;  // what enters the chunk where no rows in front of it do
     __device__ __forceinline__ void look(const RecParams &p, const Item &item, const Lane2 &l) {
         const int chunk = item.chunk;
-        needed = kBack ? chunk + 1 < p.chunks : chunk > 0;
         h = splat(0.f);
         if (item.flags & (kBack ? kEnds : kStarts)) {
             const float *from = kBack ? p.d_final : p.state;
-            needed = false;
             h = load_f32(from ? from + static_cast<size_t>(item.seq) * p.C : nullptr, l);
-        } else if (item.flags & kEdges) {
-            if (p.per_seq) {
-                needed = (kBack ? chunk + 1 : chunk) % p.per_seq != 0;
-            } else if (needed) {
-                const int row0 = item.row0, row1 = row0 + 2 * W * L, s = seq_of(p.seq, kBack ? row1 - 1 : row0);
-                needed = s >= 0 && (kBack ? row1 < seq_begin(p.seq, s + 1) : seq_begin(p.seq, s) < row0 && row0 < seq_begin(p.seq, s + 1));
-            }
         }
-        if (needed) front.read(p, chunk, kBack ? p.chunks - 1 - chunk : chunk, kBack ? -1 : 1, l);
+        if (item.flags & kNeedsFront) front.read(p, chunk, kBack ? p.chunks - 1 - chunk : chunk, kBack ? -1 : 1, l);
     }
     __device__ __forceinline__ void join(const RecParams &p, const Item &item, const float4 (*runs)[32], float2 (*start)[32],
                                          const Lane2 &l) {
-        if (item.flags & kEdges) join_runs<true, !kBack, W>(p, item.chunk, needed, h, front, runs, start, l);
-        else join_runs<false, !kBack, W>(p, item.chunk, needed, h, front, runs, start, l);
+        if (item.flags & kEdges) join_runs<true, !kBack, W>(p, item.chunk, item.flags & kNeedsFront, h, front, runs, start, l);
+        else join_runs<false, !kBack, W>(p, item.chunk, item.flags & kNeedsFront, h, front, runs, start, l);
     }
 };
 
@@ -718,7 +729,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 2) rec_plain_kernel(const __grid
         return Tile(p, nullptr, s_tiles + stage * kIn * Tile::kTensor, warp, item.tile, item.row0 + warp * 2 * L,
                     item.saved + (warp * 2 + half()) * (L / kRecRun));
     };
-    Item ahead{-1, 0, 0, 0, 0, 0};  // one thread's: the next item, taken while nothing waits for it
+    Item ahead{-1, 0, 0, 0, 0, 0, 0};  // one thread's: the next item, taken while nothing waits for it
     const auto take = [&] {
         if (threadIdx.x == W * 32) ahead = item_of(p, next_item(p, dealt), 2 * W * L, kBack);
     };
@@ -758,12 +769,12 @@ __global__ void __launch_bounds__((W + 1) * 32, 2) rec_plain_kernel(const __grid
             }
             __syncwarp();
             Tile rows = tile_of(item, n & 1);
-            if (item.flags & kEdges) {
-                const Run run = run_of<L>(p.seq, rows.row0, chunk_limit(p, item.chunk));
+            const Run run = item.flags & kEdges ? run_of<L>(p.seq, item, rows.row0, chunk_limit(p, item.chunk)) : whole_run<W>(item);
+            if (row_by_row<L>(item, run)) {
                 rows.present = present_rows<L>(run);
                 work_item_edges<W, kBack>(p, rows, run, s, s.sum[0], warp, nothing);
             } else {
-                work_item<false, W, kBack>(p, rows, whole_run<W>(item), s, s.sum[0], warp, nothing);
+                work_item<false, W, kBack>(p, rows, run, s, s.sum[0], warp, nothing);
             }
         }
         if constexpr (kBack) {
@@ -798,7 +809,7 @@ __global__ void __launch_bounds__((W + 1) * 32, kBlocks) rec_tile_kernel(const _
     const ptx::Watchdog wd{&s_abort, p.status, static_cast<uint64_t>(p.timeout_ns)};
     if (warp == W) {
         unsigned dealt = blockIdx.x;
-        Item ahead{-1, 0, 0, 0, 0, 0};  // lane 0: the item to be loaded next, taken while nothing waits for it
+        Item ahead{-1, 0, 0, 0, 0, 0, 0};  // lane 0: the item to be loaded next, taken while nothing waits for it
         auto take = [&] {
             if (lane == 0) ahead = item_of(p, next_item(p, dealt), 2 * W * L, kBack);
         };
@@ -874,10 +885,10 @@ __global__ void __launch_bounds__((W + 1) * 32, kBlocks) rec_tile_kernel(const _
         ptx::mbar_wait(&s_full[stage], parity, wd, kDevTimeoutFull);  // a failure stops the block at the joining
         const Item item = s_item[stage];
         if (item.chunk < 0) break;
-        const bool edges = item.flags & kEdges;
         const int row0 = item.row0 + warp * 2 * L;
-        const Run run = edges ? run_of<L>(p.seq, row0, chunk_limit(p, item.chunk)) : whole_run<W>(item);
+        const Run run = item.flags & kEdges ? run_of<L>(p.seq, item, row0, chunk_limit(p, item.chunk)) : whole_run<W>(item);
         Tile rows(p, q.out, s_tiles + stage * kStage, warp, item.tile, row0, item.saved + (warp * 2 + half()) * (L / kRecRun));
+        const bool edges = row_by_row<L>(item, run);
         if (edges) rows.present = present_rows<L>(run);
         if (item.chunk == 0)
             copy_empty<W>(p.seq, kBack ? p.d_final : p.state, kBack ? p.d_state : p.final_state, p.C, rows.l);

@@ -148,15 +148,15 @@ __device__ __forceinline__ int seq_begin(const Sequences &q, int s) {
 
 // The last sequence that begins at or before `row` (-1: none): with empty sequences at that
 // row, the one that holds it.
-__device__ __forceinline__ int seq_of(const Sequences &q, int row) {
+__device__ __forceinline__ int seq_of(const Sequences &q, int row, int lo, int hi) {  // known to lie in lo .. hi
     if (!q.offsets) return q.T > 0 ? min(row / q.T, q.nseq - 1) : -1;
-    int lo = -1, hi = q.nseq - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (q.offsets[mid] <= row) lo = mid; else hi = mid - 1;
     }
     return lo;
 }
+__device__ __forceinline__ int seq_of(const Sequences &q, int row) { return seq_of(q, row, -1, q.nseq - 1); }
 
 // Whether the offsets begin at 0, never fall and end inside the rows: looked at by `count` threads,
 // of which this is number `i`.  A violation is reported through the status word.
