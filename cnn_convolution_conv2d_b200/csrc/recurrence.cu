@@ -460,25 +460,38 @@ template <bool kEdge, int W, typename Rows, typename Halfway>
 __device__ __forceinline__ bool forward_item(const RecParams &p, Rows &rows, const Run &run, Joins<W, false> &s, int warp,
                                              Halfway halfway) {
     constexpr int L = Rows::kRun, kUnroll = kEdge ? 1 : L;
+    constexpr int kGroup = kEdge ? 4 : L;  // rows whose gates are worked out together
     float2 A[L], H[L];
     const float2 rate = decay_rate(p, rows.l);
 #pragma unroll kUnroll
-    for (int j = 0; j < L; ++j) {
-        if (j == L / 2) halfway();
-        const float *from = kEdge ? seq_row<L>(p.state, run, j, p.C) : nullptr;
-        if (kEdge && !(run.in >> j & 1u)) {
-            A[j] = H[j] = splat(0.f);
-            continue;
+    for (int j0 = 0; j0 < L; j0 += kGroup) {
+        float2 a[kGroup], b[kGroup];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+            const int j = j0 + i;
+            if (j == L / 2) halfway();
+            const float2 pm = exp2m1(mul2(rate, sigmoid2(rows.get(kGateA, j))));
+            b[i] = contribution(pm, sigmoid2(rows.get(kGateX, j)), rows.get(kX, j));
+            a[i] = add1(pm, 1.f);
+            if (!kEdge) {
+                A[j] = j ? mul2(A[j ? j - 1 : 0], a[i]) : a[i];
+                H[j] = j ? fma2(a[i], H[j ? j - 1 : 0], b[i]) : b[i];
+            }
         }
-        const float2 pm = exp2m1(mul2(rate, sigmoid2(rows.get(kGateA, j))));
-        const float2 b = contribution(pm, sigmoid2(rows.get(kGateX, j)), rows.get(kX, j)), a = add1(pm, 1.f);
-        if (kEdge && (run.start >> j & 1u)) {
-            A[j] = splat(0.f);
-            H[j] = fma2(a, load_f32(from, rows.l), b);
-        } else {
-            if (kEdge) A[j] = j ? product(A[j ? j - 1 : 0], no_cut(a)) : no_cut(a);
-            else A[j] = j ? mul2(A[j ? j - 1 : 0], a) : a;
-            H[j] = j ? fma2(a, H[j ? j - 1 : 0], b) : b;
+        if constexpr (kEdge) {
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) {
+                const int j = j0 + i;
+                const float *from = seq_row<L>(p.state, run, j, p.C);
+                float2 before = j ? H[j ? j - 1 : 0] : splat(0.f), kept = j ? A[j ? j - 1 : 0] : splat(1.f);
+                if (run.start >> j & 1u) {
+                    before = load_f32(from, rows.l);
+                    kept = splat(0.f);
+                }
+                const bool in = run.in >> j & 1u;
+                A[j] = in ? product(kept, no_cut(a[i])) : splat(0.f);
+                H[j] = in ? fma2(a[i], before, b[i]) : splat(0.f);
+            }
         }
     }
     const float2 all = kEdge ? A[L - 1] : no_cut(A[L - 1]);
