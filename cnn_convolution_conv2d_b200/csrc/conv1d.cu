@@ -12,6 +12,11 @@
 // tensors, a lane loads a batch of rows with one instruction, the results take the places of the rows and
 // leave the same way: half the instructions of copies and stores by every thread, which is the form for
 // other strides and alignments.
+// What the time goes into: the special-function unit (65% busy forward: an exponential and a reciprocal for each SiLU) and,
+// backward, instructions with 16 warps an SM to hide their latency (an issue slot in two is used).
+// 16384 rows of 4096 channels in bf16, K = 4, SiLU: forward 55 us (4.9 TB/s, 74% of a copy's rate), backward 102 us
+// (3.9 TB/s); without SiLU 53 and 88 us; K = 8: 72 and 174 us; 2048 channels in fp32: 55 and 84 us (4.8 TB/s); 32768 rows of
+// 1001 channels in bf16, whose rows TMA does not take: 63 and 125 us.
 #include "ptx.cuh"
 #include "sequence.cuh"
 
@@ -609,6 +614,8 @@ __global__ void __launch_bounds__(1024) conv1d_reduce_kernel(const float *partia
     }
 }
 
+// One token: a warp takes 32 * V channels of one row.  Bound by the launch and two waits for memory, one behind the other (a
+// slot's number, its window): 64 rows of 4096 channels 8 us, the launch of a graph included.
 template <typename T, int K, int V, bool kVec>
 __global__ void __launch_bounds__(128) conv1d_step_kernel(const __grid_constant__ Conv1dStepParams p) {
     const Chan<T, V, kVec> ch(blockIdx.x % p.tiles * 4 + (threadIdx.x >> 5), p.C);
