@@ -430,6 +430,69 @@ def test_streams_and_captured_graphs():
         layers[0][0](layers[0][1][0], layers[0][1][1].cpu(), layers[0][1][2])
 
 
+def test_convolution_on_streams_and_in_captured_graphs():
+    """Forward, backward and tokens of two layers at once, eager and replayed, give what they give alone."""
+    d = Draw(13, torch.bfloat16)
+    offsets = dev([0, 5, 5, 333, 600])
+    layers = [(cb.CausalConv1dB200(d(136, K)[0], d(136)[0], "silu"), d(610, 136)[0], d(610, 136)[0], d(4, K - 1, 136)[0])
+              for K in (4, 7)]
+
+    def run(layer, x, dy, state, stream=None):
+        final, window = torch.zeros_like(state), state.clone()
+        out = [layer(x, y=torch.zeros_like(x), offsets=offsets, initial_state=state, final_state=final, stream=stream), final]
+        out += layer.backward(x, dy, offsets=offsets, initial_state=state, d_final_state=state, dx=torch.zeros_like(x), stream=stream)
+        return out + [layer.step(x[:4], window, stream=stream), window]
+
+    want = [run(*l) for l in layers]
+    torch.cuda.synchronize()
+    streams, graphs, outs = [torch.cuda.Stream() for _ in layers], [], []
+    for l in layers:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run(*l))
+        graphs.append(g)
+    for _ in range(3):
+        for s, g in zip(streams, graphs):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                g.replay()
+        got = []
+        for l, s in zip(layers, streams):
+            with torch.cuda.stream(s):
+                got.append(run(*l))
+        torch.cuda.synchronize()
+        for a, b, c in zip(want, got, outs):
+            assert all(torch.equal(u, v) and torch.equal(u, w) for u, v, w in zip(a, b, c))
+    cb.conv2d_sync_status()
+
+
+def test_many_items_for_every_block():
+    """More items than blocks take at once, each kind of copy, packed and dense, twice the same bits and near one another:
+    the same rows as one batch and packed differ by the roundings of other chunks only."""
+    d = Draw(14, torch.bfloat16)
+    B, T, C = 3, 2600, 1024
+    x, ga, gx, dy = (d(B, T, C)[0] for _ in range(4))
+    rec = cb.GatedRecurrenceB200(d(C, dtype=torch.float32)[0] - 3.5)
+    offsets = dev([0, T, 2 * T, 3 * T])
+    wide = torch.empty(B, T, C + 1, dtype=torch.bfloat16, device="cuda")    # rows of 2050 bytes: no bulk copies
+    wide[..., :C] = x
+
+    def run(x, **kw):
+        flat = lambda t: t.reshape(B * T, -1) if kw else t  # noqa: E731
+        shaped = x.flatten(0, 1) if kw else x
+        saved = rec.saved_states(shaped)
+        y = rec(shaped, flat(ga), flat(gx), saved=saved, **kw)
+        return [t.reshape(B, T, C) for t in (y, *rec.backward(shaped, flat(ga), flat(gx), flat(dy), saved, **kw)[:3])]
+
+    dense, again, strided, packed = run(x), run(x), run(wide[..., :C]), run(x, offsets=offsets)
+    for a, b, c, e in zip(dense, again, strided, packed):
+        assert torch.equal(a, b) and torch.equal(a, c)
+        # both are within half a step of bf16 of fp32 results that differ by rounding errors, 2^-24 times some hundreds of terms
+        size = torch.maximum(a.float().abs(), e.float().abs())
+        assert bool(((a.float() - e.float()).abs() <= 2 ** -7 * size + 2 ** -24 * 1000 * a.float().abs().max()).all())
+    cb.conv2d_sync_status()
+
+
 def test_a_carry_that_never_comes_ends_in_a_timeout():
     x = torch.zeros(1, 300, 64, device="cuda")
     rec = cb.GatedRecurrenceB200(torch.zeros(64, device="cuda"))
