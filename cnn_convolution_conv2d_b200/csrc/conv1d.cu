@@ -17,6 +17,8 @@
 // 16384 rows of 4096 channels in bf16, K = 4, SiLU: forward 55 us (4.9 TB/s, 74% of a copy's rate), backward 102 us
 // (3.9 TB/s); without SiLU 53 and 88 us; K = 8: 72 and 174 us; 2048 channels in fp32: 55 and 84 us (4.8 TB/s); 32768 rows of
 // 1001 channels in bf16, whose rows TMA does not take: 63 and 125 us.
+#include <atomic>
+
 #include "ptx.cuh"
 #include "sequence.cuh"
 
@@ -661,8 +663,16 @@ cudaError_t backward_k(const Conv1dTiles &q, cudaStream_t s) {
     const int grid = p.tiles * (p.row_blocks + (p.d_state ? p.seq.nseq : 0));
     constexpr size_t smem = kConvWarps * kRing * 2 * (kConvBatch / sizeof(T)) * 32 * sizeof(Raw<T, V>);
     const auto kernel = conv1d_backward_kernel<T, K, V, kVec>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static std::atomic<uint64_t> allowed{0};  // a bit for each device on which the kernel may have that much
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+    if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
     kernel<<<grid, kConvWarps * 32, smem, s>>>(q);
     return cudaGetLastError();
 }

@@ -46,6 +46,12 @@ def conv1d_causal_backward_workspace_size(rows, C, K) -> int:
     return _size(load().conv1d_causal_backward_workspace_size, rows, C, K)
 
 
+@functools.lru_cache(maxsize=4096)
+def _conv_scratch_bytes(index, rows, C, K) -> int:
+    """conv1d_causal_backward_workspace_size on device `index`, the current one, on which it depends besides."""
+    return conv1d_causal_backward_workspace_size(rows, C, K)
+
+
 # These three depend on their arguments alone: asked once for each.
 @functools.lru_cache(maxsize=4096)
 def gated_recurrence_saved_size(nseq, T, rows, C, dtype) -> int:
@@ -232,7 +238,7 @@ class CausalConv1dB200:
             gb = _new(self.bias) if db is None and self.bias is not None else db
             gs = _new(initial_state) if d_initial_state is None and initial_state is not None else d_initial_state
             pgx, ldgx = _rows("dx", gx, x)
-            ws = _scratch(conv1d_causal_backward_workspace_size(seq[3], self.C, self.K), x.device)
+            ws = _scratch(_conv_scratch_bytes(x.device.index, seq[3], self.C, self.K), x.device)
             _check(load().conv1d_causal_backward(
                 px, self.w.data_ptr(), self._bias(), pdy, state, dfinal, pgx,
                 _whole("dw", gw, (self.C, self.K), x.dtype, x.device), _whole("db", gb, (self.C,), x.dtype, x.device),
