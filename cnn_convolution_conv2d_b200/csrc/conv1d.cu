@@ -18,6 +18,7 @@
 // (3.9 TB/s); without SiLU 53 and 88 us; K = 8: 72 and 174 us; 2048 channels in fp32: 55 and 84 us (4.8 TB/s); 32768 rows of
 // 1001 channels in bf16, whose rows TMA does not take: 63 and 125 us.
 #include <atomic>
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "sequence.cuh"
@@ -503,38 +504,42 @@ __global__ void __launch_bounds__(kConvWarps * 32, kConvBlocksBack) conv1d_backw
                 shift_in<K - 1, V>(past, zero_pairs<V>());
             }
         };
+        // U rows of one sequence, all of whose gradients belong to it too.  kWhole: those of the strip, sent together.
+        auto batch = [&](int row, auto whole) {
+            constexpr bool kWhole = decltype(whole)::value;
+            Pairs<V> all[K - 1 + U], dz[K - 1 + U];
+            const int target = row - (K - 1);  // the first of the rows whose gradients are finished
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {
+                all[j] = win[j];
+                dz[j] = past[j];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (u == U / 2) fetch(row + 2 * U, 2);
+                Raw<T, V> &at = ring.at(0, u);
+                all[K - 1 + u] = pairs<T, V>(at);
+                dz[K - 1 + u] = slope(pairs<T, V>(ring.at(1, u)), all + u);
+                if (kWhole || row + u < row1) sums(dz[K - 1 + u], all + u);
+                const Pairs<V> g = gradient(dz + u);
+                if (kWhole) at = pack<T, V>(g);
+                else if (target + u >= row0 && target + u < row1)  // (rows behind `last` hold nothing, and end here)
+                    store<T, V, kVec>(dx + static_cast<size_t>(target + u) * p.ldy, g, ch);
+            }
+            if (kWhole) ring.send(&q.out, tile, target);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {
+                win[j] = all[U + j];
+                past[j] = dz[U + j];
+            }
+        };
         bool done = false;
         for (int row = row0; row < last; row += U, ring.next()) {
             if (!ring.wait(p)) break;
             if (done) continue;  // (two batches at most: K-1 rows behind the strip)
             if (cur.inside(p.seq) && row + U <= cur.end && row - (K - 1) >= cur.begin) {
-                Pairs<V> all[K - 1 + U], dz[K - 1 + U];
-                const int target = row - (K - 1);  // the first of the rows whose gradients are finished
-                const bool bulk = kVec && target >= row0 && target + U <= row1;
-#pragma unroll
-                for (int j = 0; j < K - 1; ++j) {
-                    all[j] = win[j];
-                    dz[j] = past[j];
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int t = row + u;
-                    if (u == U / 2) fetch(row + 2 * U, 2);
-                    Raw<T, V> &at = ring.at(0, u);
-                    all[K - 1 + u] = pairs<T, V>(at);
-                    dz[K - 1 + u] = slope(pairs<T, V>(ring.at(1, u)), all + u);
-                    if (t < row1) sums(dz[K - 1 + u], all + u);
-                    const Pairs<V> g = gradient(dz + u);
-                    if (bulk) at = pack<T, V>(g);
-                    else if (target + u >= row0 && target + u < row1)  // (rows behind `last` hold nothing, and end here)
-                        store<T, V, kVec>(dx + static_cast<size_t>(target + u) * p.ldy, g, ch);
-                }
-                if (bulk) ring.send(&q.out, tile, target);
-#pragma unroll
-                for (int j = 0; j < K - 1; ++j) {
-                    win[j] = all[U + j];
-                    past[j] = dz[U + j];
-                }
+                if (kVec && row - (K - 1) >= row0 && row + U <= row1) batch(row, std::true_type{});
+                else batch(row, std::false_type{});
             } else {  // a sequence begins or ends here: row by row
                 fetch(row + 2 * U, 2);
 #pragma unroll 1
