@@ -57,7 +57,8 @@ CASES = [  # B, T, offsets, rows (behind the last sequence), C, K, silu, carried
     (40, 0, list(range(0, 123, 3)), 122, 33, 7, True, True),  # many short ones
     (2, 0, [0, 0, 0], 9, 16, 4, True, True),        # rows, but none of a sequence
     (2, 512, None, None, 40, 4, True, True),        # chunks that begin and end with their sequences, forward,
-    (3, 672, None, None, 33, 2, False, True),       # ... backward (672 is 6 x 112 and 7 x 96),
+    (3, 672, None, None, 33, 2, False, True),       # ... backward (672 is 7 x 96, 384 is 3 x 128 and 4 x 96),
+    (2, 384, None, None, 33, 2, False, True),
     (4, 0, [0, 256, 256, 928, 1600], 1700, 48, 3, True, True),  # ... and packed
 ]
 IDS = [f"B{c[0]}-T{c[1] if c[2] is None else 'packed'}-C{c[4]}-K{c[5]}" for c in CASES]

@@ -46,15 +46,15 @@ def test_sizes(lib):
     # without a device strips are 64 rows, four to a block: 1000 rows are 4 blocks of (K + 1) C sums
     if not torch.cuda.is_available():
         assert cb.conv1d_causal_backward_workspace_size(1000, 64, 4) == 4 * 5 * 64 * 4
-    # one chunk (forward 256 rows in bf16, 128 in fp32; backward 112 and 96): nothing to join; otherwise three values for
+    # one chunk (forward 256 rows in bf16, 128 in fp32; backward 128 and 96): nothing to join; otherwise three values for
     # each chunk and channel (rounded up to 32), and a rate; backward also a sum for each
     forward, backward, saved = (cb.gated_recurrence_workspace_size, cb.gated_recurrence_backward_workspace_size,
                                 cb.gated_recurrence_saved_size)
     assert forward(1, 0, 256, 100, BF) == 0 and forward(1, 128, 128, 100, F) == 0
     assert forward(1, 0, 257, 100, BF) == 256 + 2 * 128 * 12 + 128 * 4
     assert forward(9, 0, 257, 100, F) == 256 + 3 * 128 * 12 + 128 * 4
-    assert backward(1, 0, 112, 100, BF) == 128 * 4
-    assert backward(1, 0, 113, 100, BF) == 256 + 2 * 128 * 16 + 128 * 4
+    assert backward(1, 0, 128, 100, BF) == 128 * 4
+    assert backward(1, 0, 129, 100, BF) == 256 + 2 * 128 * 16 + 128 * 4
     assert backward(1, 0, 97, 100, F) == 256 + 2 * 128 * 16 + 128 * 4
     # a saved state for every 8 rows that have begun; sequences of a few chunks have chunks and states of their own
     assert saved(1, 129, 129, 100, BF) == saved(3, 0, 129, 100, F) == 17 * 128 * 4
