@@ -14,9 +14,9 @@
 // other strides and alignments.
 // What the time goes into: the special-function unit (65% busy forward: an exponential and a reciprocal for each SiLU) and,
 // backward, instructions with 16 warps an SM to hide their latency (an issue slot in two is used).
-// 16384 rows of 4096 channels in bf16, K = 4, SiLU: forward 55 us (4.9 TB/s, 74% of a copy's rate), backward 102 us
-// (3.9 TB/s); without SiLU 53 and 88 us; K = 8: 72 and 174 us; 2048 channels in fp32: 55 and 84 us (4.8 TB/s); 32768 rows of
-// 1001 channels in bf16, whose rows TMA does not take: 63 and 125 us.
+// 16384 rows of 4096 channels in bf16, K = 4, SiLU: forward 55 us (4.9 TB/s, 74% of a copy's rate), backward 98 us
+// (4.1 TB/s); without SiLU 53 and 86 us; K = 8: 73 and 157 us; 2048 channels in fp32: 55 and 84 us (4.8 TB/s); 32768 rows of
+// 1001 channels in bf16, whose rows TMA does not take: 63 and 124 us.
 #include <atomic>
 #include <type_traits>
 
@@ -504,7 +504,8 @@ __global__ void __launch_bounds__(kConvWarps * 32, kConvBlocksBack) conv1d_backw
                 shift_in<K - 1, V>(past, zero_pairs<V>());
             }
         };
-        // U rows of one sequence, all of whose gradients belong to it too.  kWhole: those of the strip, sent together.
+        // U rows of one sequence, all of whose gradients belong to it too.  kWhole: those of the strip, sent together
+        // (without the checks of the other form: 102 -> 98 us).
         auto batch = [&](int row, auto whole) {
             constexpr bool kWhole = decltype(whole)::value;
             Pairs<V> all[K - 1 + U], dz[K - 1 + U];
@@ -712,7 +713,7 @@ int conv1d_channels_per_block(int K) { return 32 * lane_channels(K); }
 // Rows of a warp's strip, a multiple of 8.  Forward: 64, fewer where that leaves SMs without a block.  Backward, which
 // has fewer warps on an SM: up to 128, so that the rounds of blocks on the device, each as long as a strip and what it
 // costs to begin one (some 12 rows' time), take the least together.  At 16384 rows of 4096 channels the last round of
-// strips of 64 is mostly empty: backward 115 -> 105 us, while forward, whose warps wait for memory, loses (55 -> 57 us).
+// strips of 64 is mostly empty: backward 115 -> 102 us, while forward, whose warps wait for memory, loses (55 -> 57 us).
 int conv1d_strip(int rows, int C, int K, int sms, bool back) {
     const long long tiles = (C + conv1d_channels_per_block(K) - 1) / conv1d_channels_per_block(K);
     const auto blocks = [&](int strip) { return tiles * ((rows + kConvWarps * strip - 1LL) / (kConvWarps * strip)); };
