@@ -11,6 +11,7 @@ namespace conv2d_b200 {
 namespace {
 
 constexpr long long kMaxRows = 1LL << 30;
+constexpr int kMaxChannels = 1 << 30;  // a tile's last channel stays an int
 constexpr long long kMaxBlocks = 0x7fffffffLL;
 
 int elt_bytes(conv_dtype_t dtype) { return dtype == CONV_F32 ? 4 : dtype == CONV_BF16 ? 2 : 0; }
@@ -34,7 +35,7 @@ int check_sequences(const int *offsets, int nseq, int T, long long rows, int C, 
     if (!offsets && (T < 0 || rows != static_cast<long long>(nseq) * T))
         return abi_fail(CONV_ERR_INVALID_ARG, "without offsets, rows must be nseq * T");
     if (!aligned(offsets, 4)) return abi_fail(CONV_ERR_UNSUPPORTED, "offsets must be aligned to 4 bytes");
-    if (rows > kMaxRows) return abi_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows");
+    if (rows > kMaxRows || C > kMaxChannels) return abi_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows or channels");
     return CONV_OK;
 }
 
@@ -134,7 +135,7 @@ int rec_layout(int nseq, int T, long long rows, int C, conv_dtype_t dtype, bool 
     if (nseq < 1 || T < 0 || rows < 0 || C < 1)
         return abi_fail(CONV_ERR_INVALID_ARG, "nseq and C must be at least 1, T and rows at least 0");
     if (T > 0 && rows != static_cast<long long>(nseq) * T) return abi_fail(CONV_ERR_INVALID_ARG, "rows must be nseq * T");
-    if (rows > kMaxRows) return abi_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows");
+    if (rows > kMaxRows || C > kMaxChannels) return abi_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows or channels");
     const long long chunk_rows = rec_shape(elt, back).rows(), tiles = ceil_div(C, kRecTile);
     const bool own = nseq > 1 && own_chunks(nseq, T, tiles, elt);
     r->per_seq = own ? static_cast<int>(ceil_div(T, chunk_rows)) : 0;
@@ -253,7 +254,7 @@ int conv1d_causal_forward(const void *x, const void *w, const void *bias, void *
 int conv1d_causal_backward_workspace_size(long long rows, int C, int K, size_t *bytes) {
     if (!bytes || rows < 0 || C < 1) return abi_fail(CONV_ERR_INVALID_ARG, "workspace size: invalid argument");
     RETURN_IF(check_conv(K, CONV_ACT_NONE));
-    if (rows > kMaxRows) return abi_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows");
+    if (rows > kMaxRows || C > kMaxChannels) return abi_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows or channels");
     int strip = 0;
     *bytes = static_cast<size_t>(conv_row_blocks(rows, C, K, sms_or_zero(), true, &strip)) * (K + 1) * C * sizeof(float);
     return abi_ok();
@@ -312,6 +313,7 @@ int conv1d_causal_step(const void *x, const void *w, const void *bias, void *y, 
     const int elt = elt_bytes(dtype);
     if (elt == 0) return abi_fail(CONV_ERR_INVALID_ARG, "dtype must be CONV_F32 or CONV_BF16");
     if (B < 1 || C < 1 || pool < 1) return abi_fail(CONV_ERR_INVALID_ARG, "B, pool and C must be at least 1");
+    if (C > kMaxChannels) return abi_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 channels");
     if (!slots && pool < B) return abi_fail(CONV_ERR_INVALID_ARG, "without slots, pool must be at least B");
     RETURN_IF(check_conv(K, activation));
     const int lanes = conv1d_channels_per_block(K) / 32;
@@ -446,6 +448,7 @@ int gated_recurrence_step(const void *x, const void *gate_a, const void *gate_x,
     const int elt = elt_bytes(dtype);
     if (elt == 0) return abi_fail(CONV_ERR_INVALID_ARG, "dtype must be CONV_F32 or CONV_BF16");
     if (B < 1 || C < 1 || pool < 1) return abi_fail(CONV_ERR_INVALID_ARG, "B, pool and C must be at least 1");
+    if (C > kMaxChannels) return abi_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 channels");
     if (!slots && pool < B) return abi_fail(CONV_ERR_INVALID_ARG, "without slots, pool must be at least B");
     RETURN_IF(check_rec(decay, kappa));
     bool wide = false;

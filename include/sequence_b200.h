@@ -24,7 +24,7 @@
  * - Results do not depend on timing: equal inputs give equal bits.
  * - Outputs must not overlap inputs or each other; rows may interleave in one buffer.
  * - rows = 0 is allowed (tensors over rows may then be NULL), nseq = 0 is not.
- * - CONV_ERR_UNSUPPORTED: more than 2^30 rows, or more blocks than one launch takes.
+ * - CONV_ERR_UNSUPPORTED: more than 2^30 rows or channels, or more blocks than one launch takes.
  */
 #ifndef SEQUENCE_B200_H
 #define SEQUENCE_B200_H

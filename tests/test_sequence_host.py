@@ -67,6 +67,12 @@ def test_sizes(lib):
     with pytest.raises(cb.Conv2dError) as err:
         cb.gated_recurrence_workspace_size(1, 0, 2 ** 31, 4, BF)
     assert err.value.status == cb.CONV_ERR_UNSUPPORTED
+    for size in (lambda C: saved(1, 0, 1, C, BF), lambda C: forward(1, 0, 1, C, F), lambda C: backward(1, 0, 1, C, F),
+                 lambda C: cb.conv1d_causal_backward_workspace_size(1, C, 4)):
+        size(2 ** 30)
+        with pytest.raises(cb.Conv2dError) as err:
+            size(2 ** 30 + 1)
+        assert err.value.status == cb.CONV_ERR_UNSUPPORTED
     for K in (1, 9):
         with pytest.raises(cb.Conv2dError):
             cb.conv1d_causal_backward_workspace_size(8, 8, K)
