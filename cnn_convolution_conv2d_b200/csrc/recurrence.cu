@@ -36,7 +36,7 @@
 // chains with twice the links, 197 us where these take 158 for 32768 rows of 2048 channels).
 // 16384 rows of 4096 channels in bf16: forward 141 us (3.8 TB/s), backward 278 us (3.4 TB/s); 2048 channels in fp32:
 // 100 us (5.3 TB/s) and 184 us (5.1 TB/s); one sequence of 32768 x 2048 in bf16: 158 and 297 us; 12 packed ones of 16384 x
-// 2560: 139 and 229 us; 3 x 777 x 1001 in fp32, whose rows TMA does not take: 35 and 57 us.
+// 2560: 139 and 229 us; 3 x 777 x 1001 in fp32, whose rows TMA does not take: 35 and 53 us.
 #include <atomic>
 
 #include "ptx.cuh"

@@ -112,17 +112,17 @@ struct RecLayout {
 };
 
 // Whether each of nseq sequences of T rows has chunks of its own, in both directions (they share the saved states):
-// then a chunk hardly ever waits for the one in front of it, but the last chunk of each sequence is not full.  Taken
-// where that costs an eighth at most (3 x 4777 rows of 1001 channels in fp32, forward: 125 -> 113 us), and up to half
-// where all items still run at once (8 x 100 rows of 512 channels: forward 20.4 -> 18.4 us; where they did not,
-// 5 x 200 rows of 1024 channels, backward: 28.7 -> 34.8 us).
+// then a chunk hardly ever waits for the one in front of it, and sequences begin and end with their chunks, but the last
+// chunk of each is not full.  Taken where that costs a third at most (bf16, 4 x 1100 rows of 2048 channels: 51 -> 43 and
+// 74 -> 64 us, 8 x 600 rows: 53 -> 57 and 90 -> 70 us; where it costs more, 16 x 350 rows: 66 -> 80 and 102 -> 87 us), and
+// up to half where all items still run at once (8 x 100 rows of 512 channels: forward 20.4 -> 18.4 us).
 bool own_chunks(int nseq, int T, long long tiles, int elt) {
     if (T < 1) return false;
     bool full = true, few = true;
     for (const bool back : {false, true}) {
         const RecShape shape = rec_shape(elt, back);
         const long long chunk_rows = shape.rows(), per_seq = ceil_div(T, chunk_rows);
-        full = full && 8 * per_seq * chunk_rows <= 9LL * T;
+        full = full && 3 * per_seq * chunk_rows <= 4LL * T;
         few = few && per_seq * chunk_rows <= 2LL * T && per_seq * nseq * tiles <= shape.blocks * 148;
     }
     return full || few;
