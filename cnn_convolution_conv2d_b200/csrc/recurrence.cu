@@ -406,7 +406,7 @@ __device__ __forceinline__ float2 step_over(float4 r, float2 h) {
 // The joining warp's part of an item: publishes the chunk's (A, H), finds the state that enters the chunk,
 // publishes the one that leaves it, and hands out those that enter the runs.
 template <bool kEdge, bool kForward, int W>
-__device__ __forceinline__ void join_runs(const RecParams &p, int chunk, bool needed, float2 h, Published &front,
+__device__ __forceinline__ void join_runs(const RecParams &p, int chunk, bool needed, float2 h, Published &front, bool &gave_up,
                                           const float4 (*runs)[32], float2 (*start)[32], const Lane2 &l) {
     constexpr int kStep = kForward ? 1 : -1;
     const int lane = threadIdx.x & 31;
@@ -439,7 +439,8 @@ __device__ __forceinline__ void join_runs(const RecParams &p, int chunk, bool ne
             if ((i & 63u) == 0) {
                 const uint64_t now = __shfl_sync(kFull, ptx::globaltimer_ns(), 0);
                 if (!began) began = now;
-                else if (now - began > static_cast<uint64_t>(p.timeout_ns)) {  // report, and go on with zeros
+                else if (gave_up || now - began > static_cast<uint64_t>(p.timeout_ns)) {  // report, and go on with zeros
+                    gave_up = true;  // the block's next waits are short
                     if (lane == 0) atomicExch(p.status, kDevTimeoutCarry);
                     h = splat(0.f);
                     break;
@@ -720,6 +721,8 @@ template <int W, int L, bool kBack>
 struct Joining {
     Published front;
     float2 h;  // what enters the chunk where no rows in front of it do
+    bool &gave_up;
+    __device__ explicit Joining(bool &gave_up_) : gave_up(gave_up_) {}
     __device__ __forceinline__ void look(const RecParams &p, const Item &item, const Lane2 &l) {
         const int chunk = item.chunk;
         h = splat(0.f);
@@ -731,8 +734,8 @@ struct Joining {
     }
     __device__ __forceinline__ void join(const RecParams &p, const Item &item, const float4 (*runs)[32], float2 (*start)[32],
                                          const Lane2 &l) {
-        if (item.flags & kEdges) join_runs<true, !kBack, W>(p, item.chunk, item.flags & kNeedsFront, h, front, runs, start, l);
-        else join_runs<false, !kBack, W>(p, item.chunk, item.flags & kNeedsFront, h, front, runs, start, l);
+        if (item.flags & kEdges) join_runs<true, !kBack, W>(p, item.chunk, item.flags & kNeedsFront, h, front, gave_up, runs, start, l);
+        else join_runs<false, !kBack, W>(p, item.chunk, item.flags & kNeedsFront, h, front, gave_up, runs, start, l);
     }
 };
 
@@ -761,6 +764,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 2) rec_plain_kernel(const __grid
     }
     take();
     __syncthreads();
+    bool gave_up = false;  // the joining warp's: a wait for what is in front ran out
     if (warp < W && s_item[0].chunk >= 0) tile_of(s_item[0], 0).fetch(kIn);
     for (unsigned n = 0;; ++n) {
         const Item item = s_item[n & 1];
@@ -773,7 +777,7 @@ __global__ void __launch_bounds__((W + 1) * 32, 2) rec_plain_kernel(const __grid
         auto nothing = [] {};
         if (warp == W) {
             const Lane2 l(item.tile, p.C);
-            Joining<W, L, kBack> joining;
+            Joining<W, L, kBack> joining(gave_up);
             joining.look(p, item, l);
             ptx::named_barrier(kRunsIn, kAll);
             joining.join(p, item, s.run, s.start, l);
@@ -857,7 +861,7 @@ __global__ void __launch_bounds__((W + 1) * 32, kBlocks) rec_tile_kernel(const _
         take();
         int2 one = make_int2(-1, 0);  // chunk and tile of the item before
         unsigned n = 0;
-        bool stop = false;
+        bool stop = false, gave_up = false;  // a load did not come; a wait for what is in front ran out
         for (;; ++n) {
             const Item item = s_item[n % S];
             if (item.chunk < 0) break;
@@ -865,7 +869,7 @@ __global__ void __launch_bounds__((W + 1) * 32, kBlocks) rec_tile_kernel(const _
             if (item.flags & kFirst) check_offsets(p.seq, p.status, lane, 32);
             ptx::mbar_wait(&s_free, n & 1u, wd, kDevTimeoutEmpty);
             if (n > 0) issue((n - 1) % S);
-            Joining<W, L, kBack> joining;
+            Joining<W, L, kBack> joining(gave_up);
             joining.look(p, item, l);
             ptx::named_barrier(kRunsIn, kAll);
             stop = *static_cast<volatile int *>(&s_abort) != 0;

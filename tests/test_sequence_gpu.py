@@ -509,6 +509,27 @@ def test_a_carry_that_never_comes_ends_in_a_timeout():
     cb.conv2d_sync_status()
 
 
+def test_a_block_waits_once_for_carries_that_never_come():
+    """Six items for each block, each without its carry: the first wait takes the limit, the others next to nothing."""
+    x = torch.zeros(1, 100_000, 64, device="cuda")
+    rec = cb.GatedRecurrenceB200(torch.zeros(64, device="cuda"))
+    rec(x, x, x)
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    try:
+        cb.conv2d_debug_set_watchdog(200_000_000, True)   # 200 ms
+        begin.record()
+        rec(x, x, x)
+        end.record()
+        with pytest.raises(cb.Conv2dError) as err:
+            cb.conv2d_sync_status()
+        assert err.value.status == cb.CONV_ERR_TIMEOUT
+    finally:
+        cb.conv2d_debug_set_watchdog(0, False)
+    assert 150 < begin.elapsed_time(end) < 600
+    assert bool((rec(x, x, x) == 0).all())
+    cb.conv2d_sync_status()
+
+
 def test_long_offsets_pass_32_bits():
     """Rows whose byte offsets (and element offsets) pass 2^32: a strided view whose last rows lie far out."""
     rows, C, stride = 300, 64, 1 << 24
