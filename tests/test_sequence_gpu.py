@@ -278,6 +278,31 @@ def test_what_one_sequence_holds_stays_there(poison, dtype):
 
 
 @both
+def test_rows_of_no_sequence_leave_the_sums_as_they_are(dtype):
+    """NaN behind the last sequence, in every input, and in a window of an empty one: the weights' gradients are the same bits."""
+    offsets, rows, C, K = [0, 0, 140, 400], 450, 72, 4
+    d = Draw(15, dtype)
+    x, ga, gx, dy = (d(rows, C)[0] for _ in range(4))
+    conv = cb.CausalConv1dB200(d(C, K)[0], d(C)[0], "silu")
+    rec = cb.GatedRecurrenceB200(d(C, dtype=torch.float32)[0])
+    window, state, off = d(3, K - 1, C)[0], d(3, C, dtype=torch.float32)[0], dev(offsets)
+
+    def run():
+        saved = rec.saved_states(x)
+        rec(x, ga, gx, offsets=off, saved=saved, initial_state=state)
+        return [*conv.backward(x, dy, offsets=off, initial_state=window)[1:3],
+                rec.backward(x, ga, gx, dy, saved, offsets=off, initial_state=state)[3]]
+
+    clean = run()
+    for t in (x, ga, gx, dy):
+        t[400:] = float("nan")
+    window[0], state[0] = float("nan"), float("nan")
+    for a, b in zip(clean, run()):
+        assert bool(a.isfinite().all()) and torch.equal(a, b)
+    cb.conv2d_sync_status()
+
+
+@both
 @pytest.mark.parametrize("offsets", [None, [0, 3, 400, 600]], ids=["dense", "packed"])
 @pytest.mark.parametrize("decay", [-3.5, 3.0], ids=["slow", "fast"])
 def test_nan_reaches_the_later_rows_of_its_sequence(decay, offsets, dtype):
