@@ -142,12 +142,13 @@ struct TileRun {
             *reinterpret_cast<__nv_bfloat162 *>(at(tensor, j)) = __float22bfloat162_rn(f);
         }
     }
-    // Sends the results of the first n tensors; by TMA, the tile is free once lane 0's bulk reads are done.
+    // Sends the results of the first n tensors; by TMA, the tile is free once lane 0's bulk reads are done.  (The barrier
+    // comes first also where nothing is sent: lane 0 frees the tile for the next loads, so all lanes must have read it.)
     __device__ void done(int n) {
         if constexpr (kTma) {
-            if (present != kAll) return;
             ptx::fence_proxy_async_smem();
             __syncwarp();
+            if (present != kAll) return;
             if ((threadIdx.x & 31) == 0) {
                 for (int i = 0; i < n; ++i) ptx::tma_store_2d(maps + i, first + i * kTensor, tile * kRecTile, row0);
                 ptx::bulk_commit_group();

@@ -571,3 +571,28 @@ def test_long_offsets_pass_32_bits():
     assert torch.equal(conv(x, y=y, offsets=off), conv(small, offsets=off))
     assert torch.equal(rec(x, x, x, y=y, offsets=off), rec(small, small, small, offsets=off))
     cb.conv2d_sync_status()
+
+
+@both
+def test_tiles_are_read_before_they_are_loaded_again(dtype):
+    """Sequences that leave the last chunk of each part empty, many for every block: a tile's last reads are those of its
+    rows by themselves, and the loads of a later item into its place wait for them.  Rows of other strides take copies by
+    the warps; both give the same bits, run after run."""
+    d = Draw(16, dtype)
+    B, T, C = 96, 250, 1024     # (chunks of its own for each sequence: of 256 and 2 x 128 rows in bf16, 2 x 128 and 3 x 96 in fp32)
+    x, ga, gx, dy = (d(B, T, C)[0] for _ in range(4))
+    rec = cb.GatedRecurrenceB200(d(C, dtype=torch.float32)[0] - 3.5)
+    state = d(B, C, dtype=torch.float32)[0]
+    wide = torch.empty(B, T, C + 1, dtype=dtype, device="cuda")
+    wide[..., :C] = x
+
+    def run(x):
+        saved, final = rec.saved_states(x), torch.zeros(B, C, device="cuda")
+        y = rec(x, ga, gx, initial_state=state, final_state=final, saved=saved)
+        return [y, final, *rec.backward(x, ga, gx, dy, saved, initial_state=state, d_final_state=state)]
+
+    want = run(wide[..., :C])
+    for _ in range(5):
+        for a, b in zip(want, run(x)):
+            assert torch.equal(a, b)
+    cb.conv2d_sync_status()
