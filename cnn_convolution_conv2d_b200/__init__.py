@@ -630,4 +630,4 @@ from .sequence import (CONV_ACT_NONE, CONV_ACT_SILU, CausalConv1dB200, GatedRecu
                        conv1d_causal_backward_workspace_size, gated_recurrence_backward_workspace_size,
                        gated_recurrence_saved_size, gated_recurrence_workspace_size)
 from . import optimizer  # noqa: E402
-from .optimizer import AdamWB200  # noqa: E402,F401
+from .optimizer import AdamWB200, adamw_describe_plan  # noqa: E402,F401

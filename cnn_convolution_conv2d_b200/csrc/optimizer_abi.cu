@@ -2,6 +2,7 @@
 // the launches of the AdamW kernel, kAdamTensors tensors each.  Host code only.
 #include <algorithm>
 #include <cmath>
+#include <cstdio>
 #include <new>
 #include <utility>
 #include <vector>
@@ -17,10 +18,12 @@ constexpr long long kMaxElements = 1LL << 41;  // the blocks of one tensor stay 
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-int check_tensors(const adamw_tensor_t *t, int count, int elt, int state_bits) {
+// *master: whether the tensors that have elements have master weights (those without are passed over, whatever they hold).
+int check_tensors(const adamw_tensor_t *t, int count, int elt, int state_bits, bool *master) {
     std::vector<std::pair<uintptr_t, uintptr_t>> weights;
     weights.reserve(count);
-    bool master = false, none = false;
+    bool none = false;
+    *master = false;
     for (int i = 0; i < count; ++i) {
         const adamw_tensor_t &a = t[i];
         if (a.numel < 0) return abi_fail(CONV_ERR_INVALID_ARG, "tensor %d: numel is negative", i);
@@ -34,13 +37,13 @@ int check_tensors(const adamw_tensor_t *t, int count, int elt, int state_bits) {
             !aligned16(a.exp_avg_sq) || ((reinterpret_cast<uintptr_t>(a.exp_avg_scale) |
                                           reinterpret_cast<uintptr_t>(a.exp_avg_sq_scale)) & 3u))
             return abi_fail(CONV_ERR_UNSUPPORTED, "tensor %d: device pointers must be 16-byte aligned", i);
-        if (a.master) master = true; else none = true;
+        if (a.master) *master = true; else none = true;
         if (a.master && elt == 4)
             return abi_fail(CONV_ERR_INVALID_ARG, "tensor %d: fp32 weights are their own master weights", i);
         const uintptr_t p = reinterpret_cast<uintptr_t>(a.param);
         weights.emplace_back(p, p + static_cast<uintptr_t>(a.numel) * elt);
     }
-    if (master && none) return abi_fail(CONV_ERR_INVALID_ARG, "either all or no tensors have master weights");
+    if (*master && none) return abi_fail(CONV_ERR_INVALID_ARG, "either all or no tensors have master weights");
     std::sort(weights.begin(), weights.end());
     for (size_t i = 1; i < weights.size(); ++i)
         if (weights[i].first < weights[i - 1].second)
@@ -49,6 +52,54 @@ int check_tensors(const adamw_tensor_t *t, int count, int elt, int state_bits) {
 }
 
 bool at_least_zero(double v) { return v >= 0.0 && std::isfinite(v); }
+
+int check_types(int count, const adamw_tensor_t *tensors, conv_dtype_t param_dtype, int state_bits) {
+    if (count < 0 || (count > 0 && !tensors))
+        return abi_fail(CONV_ERR_INVALID_ARG, "count must be at least 0 and tensors not NULL");
+    if (param_dtype != CONV_F32 && param_dtype != CONV_BF16)
+        return abi_fail(CONV_ERR_INVALID_ARG, "dtypes must be CONV_F32 or CONV_BF16");
+    if (state_bits != 8 && state_bits != 32) return abi_fail(CONV_ERR_INVALID_ARG, "state_bits must be 8 or 32");
+    return CONV_OK;
+}
+
+int checked_tensors(const adamw_tensor_t *tensors, int count, int elt, int state_bits, bool *master) {
+    try {
+        return check_tensors(tensors, count, elt, state_bits, master);
+    } catch (const std::bad_alloc &) {
+        return abi_fail(CONV_ERR_INVALID_ARG, "out of host memory");
+    }
+}
+
+// Batches of a block.  With 8-bit states a block takes more batches, and finds its tensor once for them, where that leaves
+// 8 blocks an SM (100 M elements: 313 -> 258 us); with 32-bit states, which wait for memory alone, that costs (422 -> 438 us).
+int batches_of(const adamw_tensor_t *tensors, int count, int state_bits, int sms) {
+    if (state_bits == 32) return 1;
+    long long elements = 0;
+    for (int k = 0; k < count; ++k) elements += std::min(tensors[k].numel, kMaxElements);
+    return static_cast<int>(std::min<long long>(std::max<long long>(elements / kAdamBatch / (8LL * std::max(sms, 1)), 1),
+                                                kAdamBatches));
+}
+
+// The next launch: the tensors from *i on, as many as one launch takes; *i moves behind them.  Its table, first blocks and
+// first place are p's; returns its blocks.
+unsigned long long next_launch(const adamw_tensor_t *tensors, int count, int state_bits, int *i, AdamParams *p) {
+    const unsigned long long per_block = static_cast<unsigned long long>(p->batches) * kAdamBatch;
+    unsigned long long blocks = 0;
+    p->count = 0;
+    p->index0 = static_cast<unsigned>(*i);
+    for (; *i < count && p->count < kAdamTensors; ++*i) {
+        const adamw_tensor_t &a = tensors[*i];
+        const unsigned long long need = (static_cast<unsigned long long>(a.numel) + per_block - 1) / per_block;
+        if (blocks + need > 0x7fffffffULL) break;
+        p->t[p->count] = AdamTensor{a.param, a.master, a.grad, a.exp_avg, a.exp_avg_sq,
+                                    state_bits == 8 ? a.exp_avg_scale : nullptr,
+                                    state_bits == 8 ? a.exp_avg_sq_scale : nullptr, a.numel};
+        p->first[p->count++] = static_cast<unsigned>(blocks);
+        blocks += need;
+    }
+    p->first[p->count] = static_cast<unsigned>(blocks);
+    return blocks;
+}
 
 }  // namespace
 }  // namespace conv2d_b200
@@ -61,11 +112,10 @@ extern "C" {
 int adamw_step(const adamw_tensor_t *tensors, int count, conv_dtype_t param_dtype, conv_dtype_t grad_dtype,
                int state_bits, double lr, double beta1, double beta2, double eps, double weight_decay, long long step,
                const long long *step_device, const float *grad_scale, unsigned seed, conv_stream_t stream) {
-    if (count < 0 || (count > 0 && !tensors))
-        return abi_fail(CONV_ERR_INVALID_ARG, "count must be at least 0 and tensors not NULL");
-    if ((param_dtype != CONV_F32 && param_dtype != CONV_BF16) || (grad_dtype != CONV_F32 && grad_dtype != CONV_BF16))
+    int st = check_types(count, tensors, param_dtype, state_bits);
+    if (st != CONV_OK) return st;
+    if (grad_dtype != CONV_F32 && grad_dtype != CONV_BF16)
         return abi_fail(CONV_ERR_INVALID_ARG, "dtypes must be CONV_F32 or CONV_BF16");
-    if (state_bits != 8 && state_bits != 32) return abi_fail(CONV_ERR_INVALID_ARG, "state_bits must be 8 or 32");
     if (!at_least_zero(lr) || !at_least_zero(eps) || !at_least_zero(weight_decay))
         return abi_fail(CONV_ERR_INVALID_ARG, "lr, eps and weight_decay must be finite and at least 0");
     if (!(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0))
@@ -74,14 +124,11 @@ int adamw_step(const adamw_tensor_t *tensors, int count, conv_dtype_t param_dtyp
     if ((reinterpret_cast<uintptr_t>(step_device) & 7u) || (reinterpret_cast<uintptr_t>(grad_scale) & 3u))
         return abi_fail(CONV_ERR_UNSUPPORTED, "step_device or grad_scale is not aligned to its element");
     const int elt = param_dtype == CONV_F32 ? 4 : 2;
-    try {
-        const int st = check_tensors(tensors, count, elt, state_bits);
-        if (st != CONV_OK) return st;
-    } catch (const std::bad_alloc &) {
-        return abi_fail(CONV_ERR_INVALID_ARG, "out of host memory");
-    }
+    bool master = false;
+    st = checked_tensors(tensors, count, elt, state_bits, &master);
+    if (st != CONV_OK) return st;
     AbiDevice dev;
-    int st = abi_device(&dev);
+    st = abi_device(&dev);
     if (st != CONV_OK) return st;
     AdamParams p{};
     p.beta1 = static_cast<float>(beta1);
@@ -103,37 +150,40 @@ int adamw_step(const adamw_tensor_t *tensors, int count, conv_dtype_t param_dtyp
     p.seed = seed;
     p.status = dev.status;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // With 8-bit states a block takes more batches, and finds its tensor once for them, where that leaves 8 blocks an SM
-    // (100 M elements: 313 -> 258 us); with 32-bit states, which wait for memory alone, that costs (422 -> 438 us).
-    long long elements = 0;
-    for (int k = 0; k < count; ++k) elements += std::min(tensors[k].numel, kMaxElements);
-    p.batches = state_bits == 32 ? 1
-                                 : static_cast<int>(std::min<long long>(std::max<long long>(elements / kAdamBatch / (8LL * dev.sms), 1),
-                                                                        kAdamBatches));
-    const unsigned long long per_block = static_cast<unsigned long long>(p.batches) * kAdamBatch;
-    int i = 0;
-    while (i < count) {
-        // the next tensors that have elements, as many as one launch takes
-        p.count = 0;
-        unsigned long long blocks = 0;
-        bool master = false;
-        p.index0 = static_cast<unsigned>(i);
-        for (; i < count && p.count < kAdamTensors; ++i) {
-            const adamw_tensor_t &a = tensors[i];
-            const unsigned long long need = (static_cast<unsigned long long>(a.numel) + per_block - 1) / per_block;
-            if (blocks + need > 0x7fffffffULL) break;
-            p.t[p.count] = AdamTensor{a.param, a.master, a.grad, a.exp_avg, a.exp_avg_sq,
-                                      state_bits == 8 ? a.exp_avg_scale : nullptr,
-                                      state_bits == 8 ? a.exp_avg_sq_scale : nullptr, a.numel};
-            p.first[p.count++] = static_cast<unsigned>(blocks);
-            master = master || a.master;
-            blocks += need;
-        }
-        p.first[p.count] = static_cast<unsigned>(blocks);
-        if (blocks == 0) continue;
+    p.batches = batches_of(tensors, count, state_bits, dev.sms);
+    for (int i = 0; i < count;) {
+        if (next_launch(tensors, count, state_bits, &i, &p) == 0) continue;
         st = abi_launch(launch_adamw(p, elt == 4, grad_dtype == CONV_F32, master, state_bits == 8, s), "AdamW");
         if (st != CONV_OK) return st;
     }
+    return abi_ok();
+}
+
+int adamw_describe_plan(const adamw_tensor_t *tensors, int count, conv_dtype_t param_dtype, int state_bits, int sms, char *buf,
+                        size_t buflen) {
+    int st = check_types(count, tensors, param_dtype, state_bits);
+    if (st != CONV_OK) return st;
+    if (!buf) return abi_fail(CONV_ERR_INVALID_ARG, "buf must not be NULL");
+    bool master = false;
+    st = checked_tensors(tensors, count, param_dtype == CONV_F32 ? 4 : 2, state_bits, &master);
+    if (st != CONV_OK) return st;
+    AdamParams p{};
+    p.batches = batches_of(tensors, count, state_bits, sms);
+    size_t at = 0;
+    const auto put = [&](const char *fmt, auto... v) {
+        const int n = at < buflen ? std::snprintf(buf + at, buflen - at, fmt, v...) : -1;
+        at = n < 0 ? buflen : at + static_cast<size_t>(n);
+    };
+    put("{\"master\": %d, \"batches\": %d, \"launches\": [", master ? 1 : 0, p.batches);
+    const char *comma = "";
+    for (int i = 0; i < count;) {
+        const unsigned long long blocks = next_launch(tensors, count, state_bits, &i, &p);
+        if (blocks == 0) continue;
+        put("%s{\"first\": %u, \"count\": %d, \"blocks\": %llu}", comma, p.index0, p.count, blocks);
+        comma = ", ";
+    }
+    put("]%s", "}");
+    if (at >= buflen) return abi_fail(CONV_ERR_INVALID_ARG, "the buffer is too small for the plan");
     return abi_ok();
 }
 

@@ -21,7 +21,17 @@ class AdamWTensor(ctypes.Structure):
 
 SIGNATURES = {
     "adamw_step": ([ctypes.POINTER(AdamWTensor), _I, _I, _I, _I, _D, _D, _D, _D, _D, _L, _P, _P, ctypes.c_uint, _P], _I),
+    "adamw_describe_plan": ([ctypes.POINTER(AdamWTensor), _I, _I, _I, _I, ctypes.c_char_p, ctypes.c_size_t], _I),
 }
+
+
+def adamw_describe_plan(table, dtype, state_bits, sms) -> dict:
+    """The launches of a step over ``table`` (an array of AdamWTensor) as a dict."""
+    import json
+    buf = ctypes.create_string_buffer(256 + 64 * len(table))
+    _check(load().adamw_describe_plan(table, len(table), dtype, state_bits, int(sms), buf, ctypes.sizeof(buf)))
+    return json.loads(buf.value.decode())
+
 
 ADAMW_QUANT = 256  # elements that share a scale in an 8-bit state
 

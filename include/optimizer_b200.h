@@ -26,7 +26,7 @@ extern "C" {
  *                    and e5m2 values in units of a scale, a power of two, for each 256 elements
  *   exp_avg_scale, exp_avg_sq_scale : (ceil(numel / 256),) fp32 for 8 bits, else NULL.  Fresh
  *                    states are codes 0 with scales 1.
- * A tensor without elements is passed over. */
+ * A tensor without elements is passed over, whatever its other members hold. */
 typedef struct {
     void *param;
     float *master;
@@ -61,6 +61,13 @@ int adamw_step(const adamw_tensor_t *tensors, int count, conv_dtype_t param_dtyp
                int state_bits, double lr, double beta1, double beta2, double eps, double weight_decay,
                long long step, const long long *step_device, const float *grad_scale, unsigned seed,
                conv_stream_t stream);
+
+/* The launches of a step, written into buf (buflen bytes, owned by the caller) as one JSON object: "master" (1: the
+ * kernel with master weights), "batches" (1024 elements each, of a block), "launches": a list of {"first", "count"
+ * (places in `tensors`), "blocks"}.  As if the device had `sms` SMs.  The pointers are checked as in
+ * adamw_step, not read; nothing runs on a GPU.  CONV_ERR_INVALID_ARG also for a NULL or too small buffer. */
+int adamw_describe_plan(const adamw_tensor_t *tensors, int count, conv_dtype_t param_dtype, int state_bits, int sms,
+                        char *buf, size_t buflen);
 
 #ifdef __cplusplus
 }

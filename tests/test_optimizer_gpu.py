@@ -198,6 +198,19 @@ def test_a_step_number_below_one_is_reported():
     assert not torch.equal(p, kept)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_tensor_without_elements_does_not_choose_the_kernel(bits):
+    """Through the C entry: an entry without elements that names master weights, beside weights that have none."""
+    p, g = normal((300,), 1, 0.1, BF), normal((300,), 2, 1.0, BF)
+    opt, alone = cb.AdamWB200([p, p[:0]], state_bits=bits), cb.AdamWB200([p.clone()], state_bits=bits)
+    decoy = torch.full((4,), 7.0, device="cuda")
+    opt._table[1].master = decoy.data_ptr()
+    opt.step([g, g[:0]])
+    alone.step([g])
+    assert torch.equal(p, alone.params[0]) and bool((decoy == 7.0).all())
+    cb.conv2d_sync_status()
+
+
 def test_refusals():
     p = [torch.zeros(16, device="cuda"), torch.zeros(16, device="cuda")]
     for bad in (lambda: cb.AdamWB200([p[0], p[0]]), lambda: cb.AdamWB200([p[0], p[0][4:12]]), lambda: cb.AdamWB200(p, state_bits=4),

@@ -177,6 +177,37 @@ def test_adamw_refusals(lib, change, status):
     assert cb.conv2d_last_error()
 
 
+def table_of(*entries):
+    table = (optimizer.AdamWTensor * len(entries))()
+    for i, (t, e) in enumerate(zip(table, entries)):
+        e = dict(dict(param=(i + 1) << 48, grad=64, exp_avg=128, exp_avg_sq=192, exp_avg_scale=256, exp_avg_sq_scale=320, numel=8), **e)
+        for k, v in e.items():
+            setattr(t, k, v)
+    return table
+
+
+def test_adamw_launches(lib):
+    """Tensors without elements are passed over whatever they hold: they do not choose the kernel, but keep their place."""
+    plan = cb.adamw_describe_plan(table_of(dict(), dict(numel=0, master=4096), dict(numel=1025)), BF, 32, 148)
+    assert plan == {"master": 0, "batches": 1, "launches": [{"first": 0, "count": 3, "blocks": 3}]}
+    plan = cb.adamw_describe_plan(table_of(dict(numel=0), dict(master=4096)), BF, 32, 148)
+    assert plan["master"] == 1 and plan["launches"] == [{"first": 0, "count": 2, "blocks": 1}]
+    assert cb.adamw_describe_plan(table_of(*[dict(numel=0, master=16, param=None)] * 3), BF, 8, 148)["launches"] == []
+    # 48 tensors of a launch, those without elements among them
+    plan = cb.adamw_describe_plan(table_of(*[dict(numel=n % 2 * 1024) for n in range(100)]), F, 32, 148)
+    assert plan["launches"] == [{"first": 0, "count": 48, "blocks": 24}, {"first": 48, "count": 48, "blocks": 24},
+                                {"first": 96, "count": 4, "blocks": 2}]
+    # more batches a block with 8-bit states: 8 blocks an SM are left
+    plan = cb.adamw_describe_plan(table_of(dict(numel=1024 * 8 * 148 * 3)), F, 8, 148)
+    assert plan["batches"] == 3 and plan["launches"][0]["blocks"] == 8 * 148
+    for bad in (lambda t: lib.adamw_describe_plan(t, 1, F, 32, 148, None, 0),
+                lambda t: lib.adamw_describe_plan(t, 1, F, 32, 148, ctypes.create_string_buffer(8), 8),
+                lambda t: lib.adamw_describe_plan(t, -1, F, 32, 148, ctypes.create_string_buffer(99), 99),
+                lambda t: lib.adamw_describe_plan(t, 1, F, 16, 148, ctypes.create_string_buffer(99), 99),
+                lambda t: lib.adamw_describe_plan(t, 1, 4, 32, 148, ctypes.create_string_buffer(99), 99)):
+        assert bad(table_of(dict())) == INVALID
+
+
 def test_layers_refuse_on_the_host(lib):
     w = torch.zeros(6, 4)
     for bad in (lambda: cb.CausalConv1dB200(torch.zeros(6)), lambda: cb.CausalConv1dB200(torch.zeros(6, 1)),
