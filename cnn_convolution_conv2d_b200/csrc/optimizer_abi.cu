@@ -14,7 +14,7 @@
 namespace conv2d_b200 {
 namespace {
 
-constexpr long long kMaxElements = 1LL << 41;  // the blocks of one tensor stay below 2^31
+constexpr long long kMaxElements = 0x7fffffffLL * kAdamBatch;  // one tensor needs at most the blocks that a launch takes
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -28,7 +28,7 @@ int check_tensors(const adamw_tensor_t *t, int count, int elt, int state_bits, b
         const adamw_tensor_t &a = t[i];
         if (a.numel < 0) return abi_fail(CONV_ERR_INVALID_ARG, "tensor %d: numel is negative", i);
         if (a.numel == 0) continue;
-        if (a.numel > kMaxElements) return abi_fail(CONV_ERR_UNSUPPORTED, "tensor %d: more than 2^41 elements", i);
+        if (a.numel > kMaxElements) return abi_fail(CONV_ERR_UNSUPPORTED, "tensor %d: more than (2^31 - 1) * 1024 elements", i);
         if (!a.param || !a.grad || !a.exp_avg || !a.exp_avg_sq)
             return abi_fail(CONV_ERR_INVALID_ARG, "tensor %d: param, grad, exp_avg and exp_avg_sq must not be NULL", i);
         if (state_bits == 8 && (!a.exp_avg_scale || !a.exp_avg_sq_scale))

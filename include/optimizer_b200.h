@@ -56,7 +56,7 @@ typedef struct {
  * A gradient that is not finite makes its own element's state NaN, no other's.
  * CONV_ERR_INVALID_ARG: count < 0, a NULL pointer, numel < 0, lr, eps or weight_decay negative
  * or not finite, a beta outside [0, 1), step < 1, state_bits other than 8 and 32, weights that
- * overlap; CONV_ERR_UNSUPPORTED: a misaligned pointer, or more than 2^41 elements. */
+ * overlap; CONV_ERR_UNSUPPORTED: a misaligned pointer, or more than (2^31 - 1) * 1024 elements. */
 int adamw_step(const adamw_tensor_t *tensors, int count, conv_dtype_t param_dtype, conv_dtype_t grad_dtype,
                int state_bits, double lr, double beta1, double beta2, double eps, double weight_decay,
                long long step, const long long *step_device, const float *grad_scale, unsigned seed,

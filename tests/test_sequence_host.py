@@ -208,6 +208,18 @@ def test_adamw_launches(lib):
         assert bad(table_of(dict())) == INVALID
 
 
+def test_the_largest_tensor_of_adamw(lib):
+    """One that needs all the blocks of a launch is taken by itself; one element more is refused, by the plan as by the step."""
+    most = (2 ** 31 - 1) * 1024
+    plan = cb.adamw_describe_plan(table_of(dict(), dict(numel=most)), F, 32, 148)
+    assert plan["launches"] == [{"first": 0, "count": 1, "blocks": 1}, {"first": 1, "count": 1, "blocks": 2 ** 31 - 1}]
+    for numel in (most + 1, 2 ** 41):
+        assert adamw(lib, entries=[dict(numel=numel)]) == UNSUPPORTED
+        with pytest.raises(cb.Conv2dError) as err:
+            cb.adamw_describe_plan(table_of(dict(numel=numel)), F, 32, 148)
+        assert err.value.status == UNSUPPORTED
+
+
 def test_layers_refuse_on_the_host(lib):
     w = torch.zeros(6, 4)
     for bad in (lambda: cb.CausalConv1dB200(torch.zeros(6)), lambda: cb.CausalConv1dB200(torch.zeros(6, 1)),
