@@ -133,6 +133,19 @@ struct TileRun {
         const uint32_t v = *reinterpret_cast<const uint32_t *>(at(tensor, j));
         return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
     }
+    // A value of the lane's own in the places of a row's two gates.
+    __device__ void keep(int j, float2 f) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float2 *>(at(kGateA, j)) = f;
+        } else {
+            *reinterpret_cast<float *>(at(kGateA, j)) = f.x;
+            *reinterpret_cast<float *>(at(kGateX, j)) = f.y;
+        }
+    }
+    __device__ float2 kept(int j) const {
+        if constexpr (sizeof(T) == 4) return *reinterpret_cast<const float2 *>(at(kGateA, j));
+        return make_float2(*reinterpret_cast<const float *>(at(kGateA, j)), *reinterpret_cast<const float *>(at(kGateX, j)));
+    }
     __device__ void put(int tensor, int j, float2 f) {
         if (kTma && present != kAll) {
             store2<T>(output(tensor) + static_cast<size_t>(row0 + half() * L + j) * stride(tensor), f, l);
@@ -210,13 +223,17 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
-// 2^y - 1 for y <= 0, exact to a few units of the result also where it is small: with
-// y = n + f, |f| <= 1/2, it is 2^n (2^f - 1) + (2^n - 1).  2^f - 1 is f times the polynomial of
+// A decay a = 2^y for y <= 0, and p = a - 1, each exact to a few units of itself: with
+// y = n + f, |f| <= 1/2, they are 2^n q + 2^n and 2^n q + (2^n - 1), q = 2^f - 1.  q is f times the polynomial of
 // degree 5 that interpolates (2^f - 1)/f at the Chebyshev points of [-1/2, 1/2] (2e-8 off).
-// A decay a = 1 + p that is a little below 1 is applied thousands of times, so an approximate
-// exponential, biased by a unit or two, would not do.  (No special-function unit is used either:
-// the sigmoids keep that one busy.)
-__device__ __forceinline__ float2 exp2m1(float2 y) {
+// A decay a little below 1 is applied thousands of times, so an approximate
+// exponential, biased by a unit or two, would not do; a small one is a factor of d_gate_a, d_decay and the state's gradient,
+// so 1 + p, exact to 2^-25 of 1 only, would not do either.  (No special-function unit is used either:
+// the sigmoids keep that one busy.)  y below -126 counts as -126: a is above 0.
+struct Decay {
+    float2 a, p;
+};
+__device__ __forceinline__ Decay decay_of(float2 y) {
     y = make_float2(max_or_nan(y.x, -126.f), max_or_nan(y.y, -126.f));
     constexpr float kRound = 12582912.f + 127.f;  // 1.5 * 2^23 and the exponent's bias: adding it leaves n + 127 in the low bits
     const float2 r = add2(y, splat(kRound));
@@ -228,7 +245,7 @@ __device__ __forceinline__ float2 exp2m1(float2 y) {
     q = fma2(f, q, splat(0.2402265f));
     q = fma2(f, q, splat(0.6931472f));
     q = mul2(f, q);
-    return fma2(s, q, add1(s, -1.f));
+    return Decay{fma2(s, q, s), fma2(s, q, add1(s, -1.f))};
 }
 
 // From p = a - 1: minus v, v = 1 - a^2.  -p (2 + p) has no cancellation.
@@ -480,9 +497,9 @@ __device__ __forceinline__ bool forward_item(const RecParams &p, Rows &rows, con
         for (int i = 0; i < kGroup; ++i) {
             const int j = j0 + i;
             if (j == L / 2) halfway();
-            const float2 pm = exp2m1(mul2(rate, sigmoid2(rows.get(kGateA, j))));
-            b[i] = contribution(pm, sigmoid2(rows.get(kGateX, j)), rows.get(kX, j));
-            a[i] = add1(pm, 1.f);
+            const Decay d = decay_of(mul2(rate, sigmoid2(rows.get(kGateA, j))));
+            b[i] = contribution(d.p, sigmoid2(rows.get(kGateX, j)), rows.get(kX, j));
+            a[i] = d.a;
             if (!kEdge) {
                 A[j] = j ? mul2(A[j ? j - 1 : 0], a[i]) : a[i];
                 H[j] = j ? fma2(a[i], H[j ? j - 1 : 0], b[i]) : b[i];
@@ -547,7 +564,8 @@ __device__ __forceinline__ bool backward_item(const RecParams &p, Rows &rows, co
     if (!kEdge && run.start) h = load_f32(p.state ? p.state + static_cast<size_t>(run.seq) * p.C : nullptr, rows.l);
     else if (!kEdge || (run.in & 1u)) h = load2<float>(p.saved + static_cast<size_t>(rows.saved) * p.Cpad, rows.l);
     const float2 rate = decay_rate(p, rows.l);
-    float2 pm[L], ra[L], rx[L], before[L];  // a - 1, the gates, h[t-1]
+    // The gates' places in the tile take h[t-1] once the gates are worked out: registers would not hold it beside a and a - 1.
+    float2 as[L], pm[L], ra[L], rx[L];  // a, a - 1, the gates
 #pragma unroll kUnroll
     for (int j = 0; j < L; ++j) {
         if (j == L / 2) halfway();
@@ -555,10 +573,12 @@ __device__ __forceinline__ bool backward_item(const RecParams &p, Rows &rows, co
         if (kEdge && !(run.in >> j & 1u)) continue;
         ra[j] = sigmoid2(rows.get(kGateA, j));
         rx[j] = sigmoid2(rows.get(kGateX, j));
-        pm[j] = exp2m1(mul2(rate, ra[j]));
+        const Decay d = decay_of(mul2(rate, ra[j]));
+        as[j] = d.a;
+        pm[j] = d.p;
         if (kEdge && (run.start >> j & 1u)) h = load_f32(from, rows.l);
-        before[j] = h;
-        h = fma2(add1(pm[j], 1.f), h, contribution(pm[j], rx[j], rows.get(kX, j)));
+        rows.keep(j, h);
+        h = fma2(d.a, h, contribution(d.p, rx[j], rows.get(kX, j)));
     }
     // g from zero behind the run, the a of the row after, and the product of all a's so far
     float2 g = splat(0.f), a = splat(0.f), B = splat(1.f);
@@ -576,7 +596,7 @@ __device__ __forceinline__ bool backward_item(const RecParams &p, Rows &rows, co
         } else {
             g = j < L - 1 ? fma2(a, g, dh) : dh;
         }
-        a = add1(pm[j], 1.f);
+        a = as[j];
         B = kEdge ? product(B, no_cut(a)) : mul2(B, a);
     }
     const float2 S = mul2(a, g);
@@ -597,7 +617,7 @@ __device__ __forceinline__ bool backward_item(const RecParams &p, Rows &rows, co
         const float2 dh = rows.get(kDy, j), x = rows.get(kX, j);
         if (kEdge && (run.end >> j & 1u)) g = add2(dh, load_f32(behind, rows.l));
         else g = j < L - 1 ? fma2(a, g, dh) : add2(dh, G);
-        a = add1(pm[j], 1.f);
+        a = as[j];
         const float2 back = mul2(a, g), ga = mul2(ra[j], back), bx = mul2(rx[j], x);
         // 1 / beta; 1e-37 under the root keeps it finite where a is 1 and ra, beta and so all but dh's share are 0
         const float2 mv = minus_v(pm[j]);
@@ -605,7 +625,7 @@ __device__ __forceinline__ bool backward_item(const RecParams &p, Rows &rows, co
         const float2 inv = make_float2(rsqrt_approx(under.x), rsqrt_approx(under.y));
         const float2 dx = mul2(mul2(g, rx[j]), negative(mul2(mv, inv)));
         const float2 dg = mul2(mul2(dx, x), one_minus(rx[j]));
-        const float2 inner = fma2(negative(mul2(a, inv)), bx, before[j]);
+        const float2 inner = fma2(negative(mul2(a, inv)), bx, rows.kept(j));
         const float2 w = mul2(ga, inner);
         sum = fma2(ga, inner, sum);
         const float2 da = mul2(mul2(natural, w), one_minus(ra[j]));
@@ -982,8 +1002,8 @@ __global__ void __launch_bounds__(kRecStepTile / 2) rec_step_kernel(const __grid
         return;
     }
     const float2 rate = make_float2(decay_rate(decay.x, p.kappa), decay_rate(decay.y, p.kappa));
-    const float2 pm = exp2m1(mul2(rate, sigmoid2(ga)));
-    const float2 h = fma2(add1(pm, 1.f), h0, contribution(pm, sigmoid2(gx), x));
+    const Decay d = decay_of(mul2(rate, sigmoid2(ga)));
+    const float2 h = fma2(d.a, h0, contribution(d.p, sigmoid2(gx), x));
     store2<T>(static_cast<T *>(p.y) + static_cast<size_t>(b) * p.ldy, h, l);
     store2<float>(state, h, l);
 }
