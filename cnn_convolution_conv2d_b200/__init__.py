@@ -531,6 +531,7 @@ class Conv2dB200:
         self.layout = _layout_code(layout)
         self.torch_dtype = w.dtype
         self.dtype = _dtype_code(w.dtype)
+        self._w, self._bias = w, bias  # the caller's; the next two may be copies of them
         self._w_oihw = w.contiguous()
         self.w_packed = conv2d_pack_weight(self._w_oihw, groups)
         self.w_packed_t = None
@@ -539,10 +540,19 @@ class Conv2dB200:
 
     def repack(self, stream=None):
         """Packs the weight tensor the layer was made from again, after it was updated in place
-        (``AdamWB200``); the bias is read where it lies if it had the weight's dtype."""
-        conv2d_pack_weight(self._w_oihw, self.groups, self.w_packed, stream)
-        if self.w_packed_t is not None:
-            conv2d_pack_weight_backward_data(self._w_oihw, self.groups, self.w_packed_t, stream)
+        (``AdamWB200``).  A bias of the weight's dtype is read where it lies; of another, it is converted again here."""
+        import torch
+
+        def call(s):
+            with torch.no_grad():
+                if self._w_oihw is not self._w:
+                    self._w_oihw.copy_(self._w)
+                if self.bias is not self._bias:
+                    self.bias.copy_(self._bias)
+            conv2d_pack_weight(self._w_oihw, self.groups, self.w_packed, s)
+            if self.w_packed_t is not None:
+                conv2d_pack_weight_backward_data(self._w_oihw, self.groups, self.w_packed_t, s)
+        sequence._on(self.w_packed, stream, call)
 
     def out_shape(self, N, H, W):
         Ho = conv2d_output_size(H, self.Kh, self.stride, self.pad, self.dilation)

@@ -255,6 +255,32 @@ def test_training_a_convolution_layer():
     cb.conv2d_sync_status()
 
 
+@pytest.mark.parametrize("other_stream", [False, True], ids=["current", "other"])
+@pytest.mark.parametrize("which", ["channels_last", "slice", "transposed", "contiguous"])
+def test_repacking_follows_the_callers_tensors(which, other_stream):
+    """Weights that are not contiguous and a bias of another dtype, updated in place: the layer's copies are made again."""
+    make = {"channels_last": lambda: normal((16, 8, 3, 3), 1, 0.1, BF).to(memory_format=torch.channels_last),
+            "slice": lambda: normal((16, 20, 3, 3), 1, 0.1, BF)[:, 4:12],
+            "transposed": lambda: normal((8, 16, 3, 3), 1, 0.1, BF).transpose(0, 1), "contiguous": lambda: normal((16, 8, 3, 3), 1, 0.1, BF)}
+    w, b = make[which](), normal((16,), 2, 0.1)
+    x, dy = normal((2, 8, 9, 9), 3, 1.0, BF), normal((2, 16, 9, 9), 4, 1.0, BF)
+    layer = cb.Conv2dB200(w, b, pad=1, layout="nchw")
+    for step in range(2):       # without and with the transposed kernel, which the first backward pass packs
+        before = layer(x)
+        w.mul_(-0.5)
+        b.add_(1.0)
+        stream = torch.cuda.Stream() if other_stream else None
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        layer.repack(stream=stream)
+        if stream is not None:
+            torch.cuda.current_stream().wait_stream(stream)
+        fresh = cb.Conv2dB200(w.clone().contiguous(), b.to(BF), pad=1, layout="nchw")
+        assert torch.equal(layer(x), fresh(x)) and not torch.equal(layer(x), before), step
+        assert torch.equal(layer.backward_data(dy, 9, 9), fresh.backward_data(dy, 9, 9)), step
+    cb.conv2d_sync_status()
+
+
 def test_a_sequence_block_from_training_to_tokens():
     """Convolution, recurrence, their gradients and AdamW as a training step uses them, on packed sequences; then a prompt
     and single tokens with the trained weights, against one pass over all of it."""
