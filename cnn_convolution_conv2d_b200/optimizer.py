@@ -54,7 +54,10 @@ class AdamWB200:
 
     The states lie in one buffer each, a tensor at a multiple of 256 elements: ``flat["m"]``, ``flat["v"]`` and, with 8
     bits, ``flat["m_scale"]``, ``flat["v_scale"]``; ``exp_avg`` and ``exp_avg_sq`` are views of them for each tensor.  Saving
-    and restoring ``flat`` and ``step_count`` saves and restores the optimizer."""
+    and restoring ``flat`` and ``step_count`` saves and restores the optimizer.
+
+    A step works on the memory that ``params``, ``masters`` and ``flat`` have then: a weight's ``data`` may be replaced, and an
+    entry of these by another tensor of its size and type.  (A captured step keeps the memory of its capture.)"""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, state_bits=32, masters=None,
                  seed=0, step_device=None):
@@ -66,26 +69,18 @@ class AdamWB200:
         self.device, self.torch_dtype, self.dtype = first.device, first.dtype, _dtype_code(first.dtype)
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
-        for p in self.params:
-            self._like(p, "a weight", first.dtype)
+        self._sizes = [p.numel() for p in self.params]
         if masters is not None and first.dtype != torch.bfloat16:
             raise ValueError("fp32 weights are their own master weights")
         if masters is True:
             masters = [p.detach().float() for p in self.params]
         self.masters = None if masters is None else list(masters)
-        if self.masters is not None:
-            if [m.numel() for m in self.masters] != [p.numel() for p in self.params]:
-                raise ValueError("masters must have the weights' sizes")
-            for m in self.masters:
-                self._like(m, "a master weight", torch.float32)
-        if _overlap(self.params + (self.masters or [])):
-            raise ValueError("two weights share memory")
+        self._check_weights()
         if step_device is not None and (step_device.dtype != torch.int64 or step_device.numel() != 1 or
                                         step_device.device != self.device):
             raise ValueError(f"step_device must be one int64 element on {self.device}")
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
         self.state_bits, self.seed, self.step_device, self.step_count = state_bits, seed, step_device, 0
-        self._sizes = [p.numel() for p in self.params]
         at, starts = 0, []
         for n in self._sizes:
             starts.append(at)
@@ -97,17 +92,60 @@ class AdamWB200:
         if state_bits == 8:
             for name in ("m_scale", "v_scale"):
                 self.flat[name] = torch.ones(at // ADAMW_QUANT, dtype=torch.float32, device=self.device)
-        views = lambda name: [self.flat[name][s:s + n] for s, n in zip(starts, self._sizes)]  # noqa: E731
-        self.exp_avg, self.exp_avg_sq = views("m"), views("v")
+        self._starts, self._flat_like = starts, {name: (t.dtype, t.numel()) for name, t in self.flat.items()}
         self._table = (AdamWTensor * len(self.params))()
-        for i, (p, start) in enumerate(zip(self.params, starts)):
-            e = self._table[i]
-            e.param, e.numel = p.data_ptr(), p.numel()
-            e.master = None if self.masters is None else self.masters[i].data_ptr()
-            e.exp_avg, e.exp_avg_sq = self.exp_avg[i].data_ptr(), self.exp_avg_sq[i].data_ptr()
-            if state_bits == 8:
-                e.exp_avg_scale = self.flat["m_scale"].data_ptr() + 4 * (start // ADAMW_QUANT)
-                e.exp_avg_sq_scale = self.flat["v_scale"].data_ptr() + 4 * (start // ADAMW_QUANT)
+        self._known = None  # the addresses in the table
+        self._fill_table()
+
+    def _views(self, name):
+        return [self.flat[name][s:s + n] for s, n in zip(self._starts, self._sizes)]
+
+    @property
+    def exp_avg(self):
+        return self._views("m")
+
+    @property
+    def exp_avg_sq(self):
+        return self._views("v")
+
+    def _check_weights(self):
+        import torch
+        for p in self.params:
+            self._like(p, "a weight", self.torch_dtype)
+        if [p.numel() for p in self.params] != self._sizes:
+            raise ValueError("the weights have other sizes than their states")
+        if self.masters is not None:
+            if [m.numel() for m in self.masters] != self._sizes:
+                raise ValueError("masters must have the weights' sizes")
+            for m in self.masters:
+                self._like(m, "a master weight", torch.float32)
+        if _overlap(self.params + (self.masters or [])):
+            raise ValueError("two weights share memory")
+
+    def _fill_table(self):
+        """Brings the table's addresses up to date; only where one has changed are the tensors looked at again."""
+        masters = self.masters or []
+        known = ([t.data_ptr() for t in self.params], [t.numel() for t in self.params], [t.data_ptr() for t in masters],
+                 [t.numel() for t in masters], [(name, t.data_ptr(), t.numel()) for name, t in self.flat.items()])
+        if known == self._known:
+            return
+        self._check_weights()
+        if self.flat.keys() != self._flat_like.keys():
+            raise ValueError(f"flat must hold {', '.join(self._flat_like)}")
+        for name, t in self.flat.items():
+            self._like(t, f"flat[{name!r}]", self._flat_like[name][0])
+            if t.dim() != 1 or t.numel() != self._flat_like[name][1]:
+                raise ValueError(f"flat[{name!r}] must have {self._flat_like[name][1]} elements in one dimension")
+        at = {name: t.data_ptr() for name, t in self.flat.items()}
+        size = 1 if self.state_bits == 8 else 4
+        for i, (e, p, n, start) in enumerate(zip(self._table, self.params, self._sizes, self._starts)):
+            e.param, e.numel = p.data_ptr(), n
+            e.master = masters[i].data_ptr() if masters else None
+            e.exp_avg, e.exp_avg_sq = at["m"] + start * size, at["v"] + start * size
+            if self.state_bits == 8:
+                e.exp_avg_scale = at["m_scale"] + 4 * (start // ADAMW_QUANT)
+                e.exp_avg_sq_scale = at["v_scale"] + 4 * (start // ADAMW_QUANT)
+        self._known = known
 
     def _like(self, t, what, dtype):
         if not t.is_cuda or t.device != self.device or not t.is_contiguous():
@@ -122,6 +160,7 @@ class AdamWB200:
         import torch
         if len(grads) != len(self.params):
             raise ValueError(f"{len(self.params)} gradients are wanted, {len(grads)} given")
+        self._fill_table()
         dtype, device, table = grads[0].dtype, self.device, self._table
         code = _dtype_code(dtype)
         for i, (g, n) in enumerate(zip(grads, self._sizes)):

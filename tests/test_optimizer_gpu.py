@@ -234,6 +234,46 @@ def test_refusals():
     assert err.value.status == cb.CONV_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_step_works_on_the_memory_of_now(bits):
+    """Weights whose data was replaced, other masters, restored states: the step takes them, and leaves the old ones alone."""
+    def make():
+        params = [normal((300, 7), 1, 0.1, BF), normal((70,), 2, 0.1, BF)]
+        return cb.AdamWB200(params, state_bits=bits, masters=True, seed=3)
+
+    grads = [normal((300, 7), 3, 1.0, BF), normal((70,), 4, 1.0, BF)]
+    opt, want = make(), make()
+    for o in (opt, want):
+        o.step(grads)
+    old = [opt.params[0].data, opt.masters[1], *opt.flat.values()]      # (alive, so that nothing else gets their memory)
+    kept = [t.clone() for t in old]
+    opt.params[0].data = opt.params[0].data.clone()
+    opt.masters[1] = opt.masters[1].clone()
+    opt.flat = {name: t.clone() for name, t in opt.flat.items()}
+    for o in (opt, want):
+        o.step(grads)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(old, kept))
+    for a, b in zip(opt.params + opt.masters + list(opt.flat.values()) + opt.exp_avg + opt.exp_avg_sq,
+                    want.params + want.masters + list(want.flat.values()) + want.exp_avg + want.exp_avg_sq):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    good = opt.params[0].data
+    for bad, error in ((good[:100].clone(), ValueError), (good.float(), TypeError), (good.t().contiguous().t(), ValueError),
+                       (good.cpu(), ValueError)):
+        opt.params[0] = bad
+        with pytest.raises(error):
+            opt.step(grads)
+    opt.params[0] = good
+    for name, bad in (("m", opt.flat["m"][:256].clone()), ("v", opt.flat["v"].float().half()), ("other", good)):
+        flat = opt.flat
+        opt.flat = dict(flat, **{name: bad})
+        with pytest.raises((ValueError, TypeError)):
+            opt.step(grads)
+        opt.flat = flat
+    assert opt.step_count == 2
+    opt.step(grads)
+    cb.conv2d_sync_status()
+
+
 def test_training_a_convolution_layer():
     """Forward, backward, AdamW and again: the layer's own gradients update the weights it packs."""
     w, b = normal((16, 8, 3, 3), 1, 0.1), normal((16,), 2, 0.1)
