@@ -174,7 +174,7 @@ class CausalConv1dB200:
 
     ``w`` is (C, K) with 2 <= K <= 8, ``bias`` (C,) or None, both bf16 or fp32 on one CUDA device;
     ``activation`` is None or "silu".  The layer reads the tensors it was given: updating
-    them in place (``AdamWB200`` does) updates the layer."""
+    them in place (``AdamWB200`` does) updates the layer, and their ``data`` may be replaced by one of the same size and type."""
 
     def __init__(self, w, bias=None, activation=None):
         if w.dim() != 2:
@@ -186,9 +186,8 @@ class CausalConv1dB200:
         self.C, self.K = int(w.shape[0]), int(w.shape[1])
         self.dtype = _dtype_code(w.dtype)
         self.torch_dtype, self.device = w.dtype, w.device
-        _whole("w", w, w.shape, w.dtype, w.device)
-        _whole("bias", bias, (self.C,), w.dtype, w.device)
-        self.w, self.bias = w, bias
+        self.w, self.bias, self._known = w, bias, None
+        self._weights()
         self.act = CONV_ACT_SILU if activation == "silu" else CONV_ACT_NONE
 
     def _input(self, x):
@@ -208,17 +207,24 @@ class CausalConv1dB200:
         px, ldx = _rows("x", x, x)
         state = _whole("initial_state", initial_state, window, x.dtype, x.device)
         final = _whole("final_state", final_state, window, x.dtype, x.device)
+        weights = self._weights()
 
         def call(s):
             out = _new(x) if y is None else y
             py, ldy = _rows("y", out, x)
-            _check(load().conv1d_causal_forward(px, self.w.data_ptr(), self._bias(), py, state, final, *seq, self.K,
+            _check(load().conv1d_causal_forward(px, *weights, py, state, final, *seq, self.K,
                                                 self.act, ldx, ldy, self.dtype, s))
             return out
         return _on(x, stream, call)
 
-    def _bias(self):
-        return None if self.bias is None else self.bias.data_ptr()
+    def _weights(self):
+        """The pointers of w and the bias, which are looked at again where their memory is not that of the last call."""
+        known = self.w.data_ptr(), None if self.bias is None else self.bias.data_ptr()
+        if known != self._known:
+            _whole("w", self.w, (self.C, self.K), self.torch_dtype, self.device)
+            _whole("bias", self.bias, (self.C,), self.torch_dtype, self.device)
+            self._known = known
+        return known
 
     def backward(self, x, dy, offsets=None, initial_state=None, d_final_state=None, dx=None, dw=None, db=None,
                  d_initial_state=None, stream=None):
@@ -231,6 +237,7 @@ class CausalConv1dB200:
         pdy, lddy = _rows("dy", dy, x)
         state = _whole("initial_state", initial_state, window, x.dtype, x.device)
         dfinal = _whole("d_final_state", d_final_state, window, x.dtype, x.device)
+        weights = self._weights()
 
         def call(s):
             gx = _new(x) if dx is None else dx
@@ -240,7 +247,7 @@ class CausalConv1dB200:
             pgx, ldgx = _rows("dx", gx, x)
             ws = _scratch(_conv_scratch_bytes(x.device.index, seq[3], self.C, self.K), x.device)
             _check(load().conv1d_causal_backward(
-                px, self.w.data_ptr(), self._bias(), pdy, state, dfinal, pgx,
+                px, *weights, pdy, state, dfinal, pgx,
                 _whole("dw", gw, (self.C, self.K), x.dtype, x.device), _whole("db", gb, (self.C,), x.dtype, x.device),
                 _whole("d_initial_state", gs, window, x.dtype, x.device), *seq, self.K, self.act, ldx, lddy, ldgx,
                 self.dtype, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), s))
@@ -258,11 +265,12 @@ class CausalConv1dB200:
         px, ldx = _rows("x", x, x)
         ps = _whole("state", state, (state.shape[0], self.K - 1, self.C), x.dtype, x.device)
         pslots = _slots(slots, B, x.device)
+        weights = self._weights()
 
         def call(s):
             out = _new(x) if y is None else y
             py, ldy = _rows("y", out, x)
-            _check(load().conv1d_causal_step(px, self.w.data_ptr(), self._bias(), py, ps, pslots, B, state.shape[0],
+            _check(load().conv1d_causal_step(px, *weights, py, ps, pslots, B, state.shape[0],
                                              self.C, self.K, self.act, ldx, ldy, self.dtype, s))
             return out
         return _on(x, stream, call)
@@ -274,14 +282,24 @@ class GatedRecurrenceB200:
     a = exp(-kappa softplus(decay) sigmoid(gate_a)), each channel by itself.
 
     ``decay`` is (C,) fp32; x and the gates are bf16 or fp32 of one shape; states are fp32.  The
-    layer reads the ``decay`` it was given: updating it in place updates the layer."""
+    layer reads the ``decay`` it was given: updating it in place updates the layer, and its ``data`` may be replaced by one of
+    the same size and type."""
 
     def __init__(self, decay, kappa=8.0):
-        import torch
         if decay.dim() != 1:
             raise ValueError("decay must be (C,)")
-        _whole("decay", decay, decay.shape, torch.float32, decay.device)
         self.decay, self.kappa, self.C, self.device = decay, float(kappa), int(decay.shape[0]), decay.device
+        self._known = None
+        self._decay()
+
+    def _decay(self):
+        """decay's pointer; decay is looked at again where its memory is not that of the last call."""
+        import torch
+        known = self.decay.data_ptr()
+        if known != self._known:
+            _whole("decay", self.decay, (self.C,), torch.float32, self.device)
+            self._known = known
+        return known
 
     def _input(self, x):
         if x.shape[-1] != self.C:
@@ -316,13 +334,14 @@ class GatedRecurrenceB200:
         state = _whole("initial_state", initial_state, (seq[1], self.C), torch.float32, x.device)
         final = _whole("final_state", final_state, (seq[1], self.C), torch.float32, x.device)
         psaved = None if saved is None else self._saved(saved, x, code)
+        pdecay = self._decay()
 
         def call(s):
             out = _new(x) if y is None else y
             py, ldy = _rows("y", out, x)
             ws = _scratch(gated_recurrence_workspace_size(*seq[1:], code), x.device)
             _check(load().gated_recurrence_forward(
-                px, pa, pg, self.decay.data_ptr(), self.kappa, py, state, final, psaved, *seq, ldx, lda, ldg, ldy, code,
+                px, pa, pg, pdecay, self.kappa, py, state, final, psaved, *seq, ldx, lda, ldg, ldy, code,
                 None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), s))
             return out
         return _on(x, stream, call)
@@ -340,6 +359,7 @@ class GatedRecurrenceB200:
         state = _whole("initial_state", initial_state, (seq[1], self.C), f32, x.device)
         dfinal = _whole("d_final_state", d_final_state, (seq[1], self.C), f32, x.device)
         psaved = self._saved(saved, x, code)
+        pdecay = self._decay()
 
         def call(s):
             gx, ga, gg = (_new(x) if t is None else t for t in (dx, d_gate_a, d_gate_x))
@@ -348,7 +368,7 @@ class GatedRecurrenceB200:
             (pgx, ldgx), (pga, ldga), (pgg, ldgg) = _rows("dx", gx, x), _rows("d_gate_a", ga, x), _rows("d_gate_x", gg, x)
             ws = _scratch(gated_recurrence_backward_workspace_size(*seq[1:], code), x.device)
             _check(load().gated_recurrence_backward(
-                px, pa, pg, self.decay.data_ptr(), self.kappa, pdy, psaved, state, dfinal, pgx, pga, pgg,
+                px, pa, pg, pdecay, self.kappa, pdy, psaved, state, dfinal, pgx, pga, pgg,
                 _whole("d_decay", gd, (self.C,), f32, x.device),
                 _whole("d_initial_state", gs, (seq[1], self.C), f32, x.device), *seq, ldx, lda, ldg, lddy, ldgx, ldga,
                 ldgg, code, ws.data_ptr(), ws.numel(), s))
@@ -366,11 +386,12 @@ class GatedRecurrenceB200:
         (px, ldx), (pa, lda), (pg, ldg) = _rows("x", x, x), _rows("gate_a", gate_a, x), _rows("gate_x", gate_x, x)
         ps = _whole("state", state, (state.shape[0], self.C), torch.float32, x.device)
         pslots = _slots(slots, B, x.device)
+        pdecay = self._decay()
 
         def call(s):
             out = _new(x) if y is None else y
             py, ldy = _rows("y", out, x)
-            _check(load().gated_recurrence_step(px, pa, pg, self.decay.data_ptr(), self.kappa, py, ps, pslots, B,
+            _check(load().gated_recurrence_step(px, pa, pg, pdecay, self.kappa, py, ps, pslots, B,
                                                 state.shape[0], self.C, ldx, lda, ldg, ldy, code, s))
             return out
         return _on(x, stream, call)

@@ -242,6 +242,31 @@ def test_layers_refuse_on_the_host(lib):
         conv(x.bfloat16())
 
 
+def test_layers_look_at_weights_whose_memory_was_replaced(lib):
+    """Another type or size behind the same tensor is refused before anything reads it; the same kind is taken."""
+    w, b, decay = torch.zeros(6, 4), torch.zeros(6), torch.zeros(6)
+    conv, rec = cb.CausalConv1dB200(w, b), cb.GatedRecurrenceB200(decay)
+    x, window, state = torch.zeros(2, 3, 6), torch.zeros(2, 3, 6), torch.zeros(2, 6)
+    row, saved = x[:, 0].contiguous(), rec.saved_states(x)
+    conv_calls = (lambda: conv(x), lambda: conv.backward(x, x), lambda: conv.step(row, window))
+    rec_calls = (lambda: rec(x, x, x), lambda: rec.backward(x, x, x, x, saved), lambda: rec.step(row, row, row, state))
+    for t, calls, bad in ((w, conv_calls, [torch.zeros(6, 4).bfloat16(), torch.zeros(6, 3), torch.zeros(4, 6).t()]),
+                          (b, conv_calls, [torch.zeros(6).bfloat16(), torch.zeros(3)]),
+                          (decay, rec_calls, [torch.zeros(6).bfloat16(), torch.zeros(5)])):
+        good = t.data
+        for other in bad:
+            t.data = other
+            for call in calls:
+                with pytest.raises(TypeError if other.dtype != torch.float32 else ValueError) as err:
+                    call()
+                assert "CUDA" not in str(err.value)
+        for other in (good.clone(), good):
+            t.data = other
+            for call in calls:
+                with pytest.raises(ValueError, match="CUDA"):       # as far as a call gets without a device
+                    call()
+
+
 def test_reference_gradients_against_differences():
     """The 64-bit reference's own gradients, against central differences of its loss."""
     gen = torch.Generator().manual_seed(3)
