@@ -542,6 +542,8 @@ class Conv2dB200:
         """Packs the weight tensor the layer was made from again, after it was updated in place
         (``AdamWB200``).  A bias of the weight's dtype is read where it lies; of another, it is converted again here."""
         import torch
+        if self._w.shape != (self.C_out, self.C_in // self.groups, self.Kh, self.Kw) or self._w.dtype != self.torch_dtype:
+            raise ValueError("the weight has another shape or dtype than the layer was made with")
 
         def call(s):
             with torch.no_grad():

@@ -321,6 +321,19 @@ def test_repacking_follows_the_callers_tensors(which, other_stream):
     cb.conv2d_sync_status()
 
 
+def test_repacking_refuses_a_weight_of_another_size_or_type():
+    w, x = normal((16, 8, 3, 3), 1, 0.1), normal((2, 8, 9, 9), 3)
+    layer = cb.Conv2dB200(w, None, pad=1, layout="nchw")
+    good, y = w.data, layer(x)
+    for bad in (normal((32, 8, 3, 3), 1), normal((16, 8, 5, 5), 1), normal((16, 8, 3, 3), 1, 0.1, BF)):
+        w.data = bad
+        with pytest.raises(ValueError):
+            layer.repack()
+    w.data = good.clone()
+    layer.repack()
+    assert torch.equal(layer(x), y)
+
+
 def test_a_sequence_block_from_training_to_tokens():
     """Convolution, recurrence, their gradients and AdamW as a training step uses them, on packed sequences; then a prompt
     and single tokens with the trained weights, against one pass over all of it."""
