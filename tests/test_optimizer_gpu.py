@@ -116,6 +116,80 @@ def test_rounding_by_chance_keeps_the_mean():
     assert abs(m - 1) <= 6 * 0.125 * (n / N) ** 0.5
 
 
+def scrambled(h):
+    """The header's mix, of 32-bit numbers held in 64."""
+    h = ((h ^ (h >> 16)) * 0x85EBCA6B) & 0xFFFFFFFF
+    h = ((h ^ (h >> 13)) * 0xC2B2AE35) & 0xFFFFFFFF
+    return h ^ (h >> 16)
+
+
+def held_in_8_bits(x, bits, top, small, keep):
+    """(values, scales) of fp32 x: the scale brings the largest of 256 into [2^top, 2^(top+1)); then `keep` fraction bits, or steps of
+    2^(small-keep) below 2^small, up where the fraction of a step and the 16 random bits in units of 2^-16 come to one."""
+    big = torch.nn.functional.pad(x.abs(), (0, -x.numel() % 256)).view(-1, 256).amax(1)
+    scale = torch.where(big > 0, 2.0 ** (torch.frexp(big)[1] - 1 - top).double(), torch.ones_like(big).double())
+    wide = scale.repeat_interleave(256)[:x.numel()]
+    y = x.double() / wide
+    size = y.abs()
+    step = 2.0 ** ((torch.frexp(size)[1] - 1).clamp(min=small) - keep).double()
+    # the fraction counts in units of 2^-16 of a step and below; the bits of an fp32 sum above 2^small hold it
+    size = torch.where(size < 2.0 ** small, (size.float() + 2.0 ** small).double() - 2.0 ** small, size)
+    held = torch.floor(size / step + bits.double() / 65536) * step
+    return torch.copysign(held, y), scale
+
+
+@pytest.mark.parametrize("gtype", [F32, BF], ids=["f32", "bf16"])
+def test_8_bit_states_are_what_the_header_says(gtype):
+    """Bit for bit: m and v in fp32, each product and sum rounded by itself, then rounded by the hash of seed, step, place and
+    element; more tensors than one launch takes, one of them without elements, sizes that are no multiples of 256."""
+    shapes = [(n,) for n in (1, 255, 257, 0, 1000, 2049)] * 9
+    params = [normal(s, i) for i, s in enumerate(shapes)]
+    b1, b2, seed = 0.9, 0.999, 77
+    opt = cb.AdamWB200(params, betas=(b1, b2), state_bits=8, seed=seed)
+    one = lambda v: torch.tensor(v, dtype=torch.float64).float()  # noqa: E731
+    held = [(torch.zeros(s), torch.zeros(s)) for s in shapes]
+    for step in (1, 2, 3):
+        # sizes over many binades, so that some values fall below the smallest normal number of a block
+        grads = [(normal(s, 100 * step + i) * torch.exp2(normal(s, 500 + i, 4.0))).to(gtype) for i, s in enumerate(shapes)]
+        opt.step(grads)
+        for i, (g, (m, v)) in enumerate(zip(grads, held)):
+            if not g.numel():
+                continue
+            g = g.float().cpu()
+            m = m * one(b1) + g * one(1 - b1)
+            v = v * one(b2) + (g * g) * one(1 - b2)
+            key = scrambled(torch.tensor((seed + 0x9E3779B9 * step) & 0xFFFFFFFF)) + 0x85EBCA77 * (i + 1)
+            h = scrambled((torch.arange(g.numel()) * 0x9E3779B1 + scrambled(key & 0xFFFFFFFF)) & 0xFFFFFFFF)
+            hm, scale_m = held_in_8_bits(m, h & 0xFFFF, 7, -6, 3)
+            hv, scale_v = held_in_8_bits(v, h >> 16, 14, -14, 2)
+            hv = torch.where((v > 0) & (hv == 0), torch.tensor(2.0 ** -16, dtype=torch.float64), hv)
+            start, blocks = opt.exp_avg[i].storage_offset() // 256, -(-g.numel() // 256)
+            assert torch.equal(opt.flat["m_scale"][start:start + blocks].double().cpu(), scale_m), (step, i)
+            assert torch.equal(opt.flat["v_scale"][start:start + blocks].double().cpu(), scale_v), (step, i)
+            assert torch.equal(opt.exp_avg[i].double().cpu(), hm), (step, i)
+            assert torch.equal(opt.exp_avg_sq[i].double().cpu(), hv), (step, i)
+            expand = lambda t: t.repeat_interleave(256)[:g.numel()]  # noqa: E731, B023
+            held[i] = (hm * expand(scale_m)).float(), (hv * expand(scale_v)).float()
+    cb.conv2d_sync_status()
+
+
+def test_the_mean_of_rounding_by_chance():
+    """A constant gradient, v = 1 - beta2^n.  A step moves v by d = (1 - beta2) (1 - v), less than a code step s <= v / 4 of which it
+    is taken whole with the chance d / s: a variance of at most s d.  They add up to less than the sum of v (1 - beta2) / 4; the
+    mean of N elements is held to 6 deviations, and to the 2^-16 of a code step by which 16 random bits may round the chance."""
+    N, n, beta2 = 1 << 16, 400, 0.999
+    p = torch.zeros(N, device="cuda")
+    opt = cb.AdamWB200([p], lr=0.0, weight_decay=0.0, state_bits=8, seed=11)
+    g = [torch.ones(N, device="cuda")]
+    variance = 0.0
+    for step in range(1, n + 1):
+        opt.step(g)
+        variance += (1 - beta2 ** step) / 4 * (1 - beta2)
+    want = 1 - beta2 ** n
+    v = held_state(opt, 0, "v").mean().item()
+    assert abs(v - want) <= 6 * (variance / N) ** 0.5 + n * 2.0 ** -16 * want / 4
+
+
 def test_equal_seeds_give_equal_bits_and_the_device_counter_the_same_steps():
     def run(seed, device_counter, graph=False):
         params = [normal((300, 40), 1), normal((77,), 2)]

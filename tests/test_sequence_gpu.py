@@ -596,3 +596,39 @@ def test_tiles_are_read_before_they_are_loaded_again(dtype):
         for a, b in zip(want, run(x)):
             assert torch.equal(a, b)
     cb.conv2d_sync_status()
+
+
+@both
+@pytest.mark.parametrize("case", [
+    (2, 300, None, None, 128, 7, True, True), (3, 130, None, None, 192, 8, False, True), (1, 257, None, None, 72, 5, True, False),
+    (4, 0, [0, 5, 5, 300, 333], 340, 64, 8, True, True), (3, 0, [0, 3, 9, 150], None, 130, 6, True, True),
+], ids=str)
+def test_convolution_with_long_kernels(case, dtype):
+    """K of 5 to 8 in rows that travel by bulk copies (channels a multiple of 8), and one whose rows do not in bf16."""
+    test_convolution(case, dtype)
+
+
+@both
+def test_masked_gates_across_chunks(dtype):
+    """The state passes chunks (of 256 rows at most) of nothing but masked rows unchanged, and so does its gradient."""
+    C, T = 64, 700
+    d = Draw(17, dtype)
+    x, ga, gx, dy = (d(1, T, C) for _ in range(4))
+    decay, state = d(C, dtype=torch.float32), d(1, C, dtype=torch.float32)
+    for t in ga:
+        t[:, 50:] = float("-inf")
+    rec = cb.GatedRecurrenceB200(decay[0])
+    saved, final = rec.saved_states(x[0]), torch.zeros(1, C, device="cuda")
+    h = rec(x[0], ga[0], gx[0], initial_state=state[0], saved=saved, final_state=final)
+    dx, dga, dgx, dd, ds = rec.backward(x[0], ga[0], gx[0], dy[0], saved, initial_state=state[0])
+    cb.conv2d_sync_status()
+    wide = state[1].requires_grad_()
+    want, last, error = ref.recurrence(*(t[1][0] for t in (x, ga, gx)), decay[1], KAPPA, [(0, T)], wide)
+    ref.close(h[0], want, dtype, error, "y")
+    ref.close(final, last, torch.float32, error[-1], "final state")
+    # behind the first chunk the decays' products are 1 and what they add is 0: every row has the same bits
+    assert torch.equal(h[:, 256:], h[:, 256:257].expand(-1, T - 256, -1))
+    for g in (dx, dga, dgx):
+        assert bool((g[:, 50:] == 0).all()) and bool(g.isfinite().all())
+    assert bool(dd.isfinite().all())
+    ref.grad_close(ds, torch.autograd.grad((want * dy[1][0]).sum(), wide)[0], torch.float32, "d_initial_state")
