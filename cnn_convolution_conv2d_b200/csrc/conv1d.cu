@@ -12,11 +12,13 @@
 // tensors, a lane loads a batch of rows with one instruction, the results take the places of the rows and
 // leave the same way: half the instructions of copies and stores by every thread, which is the form for
 // other strides and alignments.
-// What the time goes into: the special-function unit (65% busy forward: an exponential and a reciprocal for each SiLU) and,
-// backward, instructions with 16 warps an SM to hide their latency (an issue slot in two is used).
+// What the time goes into: forward, the rows' travel: with K = 2 and no SiLU it takes 51 us of the 55 below (a copy of those
+// bytes takes 41), while the special-function unit is 65% busy and not the limit.  Backward the
+// same least work takes 82 us (its bytes 62, with K-1 rows read twice a strip, the sums' reduction and 16 warps an SM); what bf16
+// takes above that, up to 98, are instructions whose latency so few warps do not hide (an issue slot in two is used).
 // 16384 rows of 4096 channels in bf16, K = 4, SiLU: forward 55 us (4.9 TB/s, 74% of a copy's rate), backward 98 us
-// (4.1 TB/s); without SiLU 53 and 86 us; K = 8: 73 and 157 us; 2048 channels in fp32: 55 and 84 us (4.8 TB/s); 32768 rows of
-// 1001 channels in bf16, whose rows TMA does not take: 63 and 124 us.
+// (4.1 TB/s); without SiLU 53 and 86 us; K = 8: 74 and 158 us; 2048 channels in fp32: 55 and 82 us (4.9 TB/s); 32768 rows of
+// 1001 channels in bf16, whose rows TMA does not take: 61 and 121 us.
 #include <atomic>
 #include <type_traits>
 

@@ -30,13 +30,14 @@
 // back from the same places in shared memory: with loads and stores of its own each thread spent
 // more on addresses than on the recurrence.  Tensors whose base or row stride is no multiple of
 // 16 bytes take the same item code with copies by the warps.
-// What the time goes into: about 70 instructions for a lane's two channels, backward 140 (an issue slot in two is used), the special-
-// function unit (56% busy forward), 18 warps an SM that wait for one another at the joining, and with one long sequence
+// What the time goes into: about 70 instructions for a lane's two channels, backward 140 (not quite an issue slot in two is used), the
+// special-function unit (56% busy forward), 18 warps an SM that wait for one another at the joining, and with one long sequence
 // the chain of states, a link some 0.7 us.  So tiles are narrow and chunks long (64 channels of half the rows: half as many
-// chains with twice the links, 197 us where these take 158 for 32768 rows of 2048 channels).
-// 16384 rows of 4096 channels in bf16: forward 141 us (3.8 TB/s), backward 278 us (3.4 TB/s); 2048 channels in fp32:
-// 100 us (5.3 TB/s) and 184 us (5.1 TB/s); one sequence of 32768 x 2048 in bf16: 158 and 297 us; 12 packed ones of 16384 x
-// 2560: 139 and 229 us; 3 x 777 x 1001 in fp32, whose rows TMA does not take: 35 and 53 us.
+// chains with twice the links, 197 us where these took 158 for 32768 rows of 2048 channels).
+// 16384 rows of 4096 channels in bf16: forward 143 us (3.7 TB/s), backward 282 us (3.3 TB/s); 2048 channels in fp32:
+// 100 us (5.3 TB/s) and 194 us (4.8 TB/s); one sequence of 32768 x 2048 in bf16: 160 and 293 us; 12 packed ones of 16384 x
+// 2560: 139 and 223 us; 3 x 777 x 1001 in fp32, whose rows TMA does not take: 35 and 51 us.  (With a formed as
+// 1 + p these took 141 and 279, 100 and 184 us, and the gradients of fast decays were wrong.)
 #include <atomic>
 
 #include "ptx.cuh"

@@ -108,9 +108,9 @@ constexpr int kRecStepTile = 256; // channels of a block of its step
 constexpr int kRecRun = 8;        // rows of one saved state
 
 // How a kernel of the recurrence is laid out: working warps, rows that half of one scans, stages of shared memory,
-// blocks an SM.  With 8 warps (and the joining one) a thread has 96 registers, with 6 or 7 it has 128: bf16 backward 278 us
-// with 8 against 285 us with 7 (16384 x 4096), forward 141 against 164 us; fp32 backward 184 us with 6 against
-// 250 us with 7 (16384 x 2048; shared memory then holds one block an SM).
+// blocks an SM.  With 8 warps (and the joining one) a thread has 96 registers, with 6 or 7 it has 128: bf16 backward 281 us
+// with 8 against 303 us with 7 (16384 x 4096), forward 143 against 164 us; fp32 backward 194 us with 6 against
+// 283 us with 7 (16384 x 2048; shared memory then holds one block an SM).
 struct RecShape {
     int warps, run, stages, blocks;
     constexpr int rows() const { return 2 * warps * run; }

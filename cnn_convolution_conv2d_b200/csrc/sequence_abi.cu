@@ -13,6 +13,7 @@ namespace {
 constexpr long long kMaxRows = 1LL << 30;
 constexpr int kMaxChannels = 1 << 30;  // a tile's last channel stays an int
 constexpr long long kMaxBlocks = 0x7fffffffLL;
+constexpr int kSms = 148;  // a B200's: the layout of what a forward pass saves depends on the arguments alone
 
 int elt_bytes(conv_dtype_t dtype) { return dtype == CONV_F32 ? 4 : dtype == CONV_BF16 ? 2 : 0; }
 
@@ -113,9 +114,11 @@ struct RecLayout {
 
 // Whether each of nseq sequences of T rows has chunks of its own, in both directions (they share the saved states):
 // then a chunk hardly ever waits for the one in front of it, and sequences begin and end with their chunks, but the last
-// chunk of each is not full.  Taken where that costs a third at most (bf16, 4 x 1100 rows of 2048 channels: 51 -> 43 and
-// 74 -> 64 us, 8 x 600 rows: 53 -> 57 and 90 -> 70 us; where it costs more, 16 x 350 rows: 66 -> 80 and 102 -> 87 us), and
-// up to half where all items still run at once (8 x 100 rows of 512 channels: forward 20.4 -> 18.4 us).
+// chunk of each is not full.  Taken where that costs a third at most (bf16, rows of 2048 channels, forward and backward,
+// without and with: 4 x 1100 rows 51 -> 44 and 70 -> 59 us, 4 x 1030 49 -> 43 and 66 -> 61 us, 8 x 600 55 -> 57 and
+// 88 -> 70 us; fp32, 8 x 420 rows 45 -> 45 and 74 -> 64 us; where it costs more, 16 x 350 rows in bf16: 66 -> 80 and
+// 98 -> 84 us, a loss for a forward pass alone), and up to half where all items still run at once (fp32, 8 x 100 rows of 512
+// channels: 20.4 -> 16.4 and 24.6 -> 22.5 us; where they do not, 16 x 150 rows of 2048 in bf16: 47 -> 59 and 51 -> 64 us).
 bool own_chunks(int nseq, int T, long long tiles, int elt) {
     if (T < 1) return false;
     bool full = true, few = true;
@@ -123,7 +126,7 @@ bool own_chunks(int nseq, int T, long long tiles, int elt) {
         const RecShape shape = rec_shape(elt, back);
         const long long chunk_rows = shape.rows(), per_seq = ceil_div(T, chunk_rows);
         full = full && 3 * per_seq * chunk_rows <= 4LL * T;
-        few = few && per_seq * chunk_rows <= 2LL * T && per_seq * nseq * tiles <= shape.blocks * 148;
+        few = few && per_seq * chunk_rows <= 2LL * T && per_seq * nseq * tiles <= shape.blocks * kSms;
     }
     return full || few;
 }
