@@ -42,6 +42,15 @@ def _overlap(tensors):
     return any(b[0] < a[1] for a, b in zip(spans, spans[1:]))
 
 
+def _facts(tensors):
+    """What decides whether tensors can be used, a list each: addresses (which tell the device), sizes, types, contiguity.  One
+    loop for each, not for each tensor, since most of a step of many small tensors is spent here."""
+    import torch
+    t = torch.Tensor
+    return [list(map(t.data_ptr, tensors)), list(map(t.numel, tensors)), [v.dtype for v in tensors],
+            list(map(t.is_contiguous, tensors))]
+
+
 class AdamWB200:
     """AdamW for ``params``: contiguous, 16-byte aligned CUDA tensors of one dtype (bf16 or fp32) on one device.
 
@@ -94,7 +103,9 @@ class AdamWB200:
                 self.flat[name] = torch.ones(at // ADAMW_QUANT, dtype=torch.float32, device=self.device)
         self._starts, self._flat_like = starts, {name: (t.dtype, t.numel()) for name, t in self.flat.items()}
         self._table = (AdamWTensor * len(self.params))()
-        self._known = None  # the addresses in the table
+        self._entries = list(self._table)  # (views: an index into the array makes one each time)
+        self._known = None  # what the tensors in the table were
+        self._grad_addresses, self._grad_devices = None, [self.device.index] * len(self.params)
         self._fill_table()
 
     def _views(self, name):
@@ -123,10 +134,10 @@ class AdamWB200:
             raise ValueError("two weights share memory")
 
     def _fill_table(self):
-        """Brings the table's addresses up to date; only where one has changed are the tensors looked at again."""
+        """Brings the table's addresses up to date; only where a tensor has changed are they looked at again."""
         masters = self.masters or []
-        known = ([t.data_ptr() for t in self.params], [t.numel() for t in self.params], [t.data_ptr() for t in masters],
-                 [t.numel() for t in masters], [(name, t.data_ptr(), t.numel()) for name, t in self.flat.items()])
+        known = (_facts(self.params), masters and _facts(masters),
+                 [(name, t.data_ptr(), t.dtype, t.shape, t.is_contiguous()) for name, t in self.flat.items()])
         if known == self._known:
             return
         self._check_weights()
@@ -138,7 +149,7 @@ class AdamWB200:
                 raise ValueError(f"flat[{name!r}] must have {self._flat_like[name][1]} elements in one dimension")
         at = {name: t.data_ptr() for name, t in self.flat.items()}
         size = 1 if self.state_bits == 8 else 4
-        for i, (e, p, n, start) in enumerate(zip(self._table, self.params, self._sizes, self._starts)):
+        for i, (e, p, n, start) in enumerate(zip(self._entries, self.params, self._sizes, self._starts)):
             e.param, e.numel = p.data_ptr(), n
             e.master = masters[i].data_ptr() if masters else None
             e.exp_avg, e.exp_avg_sq = at["m"] + start * size, at["v"] + start * size
@@ -163,10 +174,19 @@ class AdamWB200:
         self._fill_table()
         dtype, device, table = grads[0].dtype, self.device, self._table
         code = _dtype_code(dtype)
-        for i, (g, n) in enumerate(zip(grads, self._sizes)):
-            if g.numel() != n or g.dtype != dtype or g.device != device or not g.is_contiguous():
-                raise ValueError(f"gradient {i} must be a contiguous {dtype} tensor of {n} elements on {device}")
-            table[i].grad = g.data_ptr()
+        count = len(grads)
+        addresses, *facts = _facts(grads)
+        moved = addresses != self._grad_addresses
+        # (devices share one range of addresses, so the same ones as at the last step are where they were; the first one is looked
+        # at all the same)
+        devices = list(map(torch.Tensor.get_device, grads)) if moved or grads[0].device != device else self._grad_devices
+        if facts != [self._sizes, [dtype] * count, [True] * count] or devices != self._grad_devices:
+            i = next(i for i, f in enumerate(zip(*facts, devices)) if f != (self._sizes[i], dtype, True, device.index))
+            raise ValueError(f"gradient {i} must be a contiguous {dtype} tensor of {self._sizes[i]} elements on {device}")
+        if moved:
+            for e, address in zip(self._entries, addresses):
+                e.grad = address
+            self._grad_addresses = addresses
         scale = None
         if grad_scale is not None:
             if grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or grad_scale.device != device:

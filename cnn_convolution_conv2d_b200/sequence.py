@@ -100,6 +100,19 @@ def _new(x):
     return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
+def _out(name, t, like):
+    """(tensor, pointer, row stride) of an output over rows: t, or where there is none a new one like `like`, which needs no checks."""
+    if t is None:
+        t = _new(like)
+        return t, t.data_ptr(), like.shape[-1]
+    return (t, *_rows(name, t, like))
+
+
+def _kind(t):
+    """What of a tensor decides whether it can still be used as it was: compared at each call, for less than _whole costs."""
+    return None if t is None else (t.data_ptr(), t.dtype, t.shape, t.is_contiguous())
+
+
 def _whole(name, t, shape, dtype, device):
     """Pointer of a contiguous tensor of exactly this shape and type (None: no tensor)."""
     if t is None:
@@ -210,21 +223,20 @@ class CausalConv1dB200:
         weights = self._weights()
 
         def call(s):
-            out = _new(x) if y is None else y
-            py, ldy = _rows("y", out, x)
+            out, py, ldy = _out("y", y, x)
             _check(load().conv1d_causal_forward(px, *weights, py, state, final, *seq, self.K,
                                                 self.act, ldx, ldy, self.dtype, s))
             return out
         return _on(x, stream, call)
 
     def _weights(self):
-        """The pointers of w and the bias, which are looked at again where their memory is not that of the last call."""
-        known = self.w.data_ptr(), None if self.bias is None else self.bias.data_ptr()
+        """The pointers of w and the bias, which are looked at again where they are not what they were at the last call."""
+        known = w, bias = _kind(self.w), _kind(self.bias)
         if known != self._known:
             _whole("w", self.w, (self.C, self.K), self.torch_dtype, self.device)
             _whole("bias", self.bias, (self.C,), self.torch_dtype, self.device)
             self._known = known
-        return known
+        return w[0], bias and bias[0]
 
     def backward(self, x, dy, offsets=None, initial_state=None, d_final_state=None, dx=None, dw=None, db=None,
                  d_initial_state=None, stream=None):
@@ -240,11 +252,10 @@ class CausalConv1dB200:
         weights = self._weights()
 
         def call(s):
-            gx = _new(x) if dx is None else dx
+            gx, pgx, ldgx = _out("dx", dx, x)
             gw = _new(self.w) if dw is None else dw
             gb = _new(self.bias) if db is None and self.bias is not None else db
             gs = _new(initial_state) if d_initial_state is None and initial_state is not None else d_initial_state
-            pgx, ldgx = _rows("dx", gx, x)
             ws = _scratch(_conv_scratch_bytes(x.device.index, seq[3], self.C, self.K), x.device)
             _check(load().conv1d_causal_backward(
                 px, *weights, pdy, state, dfinal, pgx,
@@ -268,8 +279,7 @@ class CausalConv1dB200:
         weights = self._weights()
 
         def call(s):
-            out = _new(x) if y is None else y
-            py, ldy = _rows("y", out, x)
+            out, py, ldy = _out("y", y, x)
             _check(load().conv1d_causal_step(px, *weights, py, ps, pslots, B, state.shape[0],
                                              self.C, self.K, self.act, ldx, ldy, self.dtype, s))
             return out
@@ -293,13 +303,13 @@ class GatedRecurrenceB200:
         self._decay()
 
     def _decay(self):
-        """decay's pointer; decay is looked at again where its memory is not that of the last call."""
+        """decay's pointer; decay is looked at again where it is not what it was at the last call."""
         import torch
-        known = self.decay.data_ptr()
+        known = _kind(self.decay)
         if known != self._known:
             _whole("decay", self.decay, (self.C,), torch.float32, self.device)
             self._known = known
-        return known
+        return known[0]
 
     def _input(self, x):
         if x.shape[-1] != self.C:
@@ -337,8 +347,7 @@ class GatedRecurrenceB200:
         pdecay = self._decay()
 
         def call(s):
-            out = _new(x) if y is None else y
-            py, ldy = _rows("y", out, x)
+            out, py, ldy = _out("y", y, x)
             ws = _scratch(gated_recurrence_workspace_size(*seq[1:], code), x.device)
             _check(load().gated_recurrence_forward(
                 px, pa, pg, pdecay, self.kappa, py, state, final, psaved, *seq, ldx, lda, ldg, ldy, code,
@@ -362,10 +371,11 @@ class GatedRecurrenceB200:
         pdecay = self._decay()
 
         def call(s):
-            gx, ga, gg = (_new(x) if t is None else t for t in (dx, d_gate_a, d_gate_x))
+            gx, pgx, ldgx = _out("dx", dx, x)
+            ga, pga, ldga = _out("d_gate_a", d_gate_a, x)
+            gg, pgg, ldgg = _out("d_gate_x", d_gate_x, x)
             gd = _new(self.decay) if d_decay is None else d_decay
             gs = _new(initial_state) if d_initial_state is None and initial_state is not None else d_initial_state
-            (pgx, ldgx), (pga, ldga), (pgg, ldgg) = _rows("dx", gx, x), _rows("d_gate_a", ga, x), _rows("d_gate_x", gg, x)
             ws = _scratch(gated_recurrence_backward_workspace_size(*seq[1:], code), x.device)
             _check(load().gated_recurrence_backward(
                 px, pa, pg, pdecay, self.kappa, pdy, psaved, state, dfinal, pgx, pga, pgg,
@@ -389,8 +399,7 @@ class GatedRecurrenceB200:
         pdecay = self._decay()
 
         def call(s):
-            out = _new(x) if y is None else y
-            py, ldy = _rows("y", out, x)
+            out, py, ldy = _out("y", y, x)
             _check(load().gated_recurrence_step(px, pa, pg, pdecay, self.kappa, py, ps, pslots, B,
                                                 state.shape[0], self.C, ldx, lda, ldg, ldy, code, s))
             return out

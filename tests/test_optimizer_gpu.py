@@ -337,6 +337,13 @@ def test_a_step_works_on_the_memory_of_now(bits):
         with pytest.raises(error):
             opt.step(grads)
     opt.params[0] = good
+    kind = opt.params[0].data
+    for other, error in ((kind.view(torch.float16), TypeError), (kind.view(7, 300).t(), ValueError)):     # in the same memory
+        assert other.data_ptr() == kind.data_ptr()
+        opt.params[0] = other
+        with pytest.raises(error):
+            opt.step(grads)
+    opt.params[0] = kind
     for name, bad in (("m", opt.flat["m"][:256].clone()), ("v", opt.flat["v"].float().half()), ("other", good)):
         flat = opt.flat
         opt.flat = dict(flat, **{name: bad})

@@ -267,6 +267,23 @@ def test_layers_look_at_weights_whose_memory_was_replaced(lib):
                     call()
 
 
+def test_layers_look_at_weights_that_changed_in_the_same_memory(lib):
+    """Memory that was freed in between may come back at the same address for another type or shape."""
+    w, decay = torch.zeros(6, 4), torch.zeros(6)
+    conv, rec = cb.CausalConv1dB200(w), cb.GatedRecurrenceB200(decay)
+    x = torch.zeros(2, 3, 6)
+    for t, call, others in ((w, lambda: conv(x), [w.data.view(torch.bfloat16), w.data[:3], w.data.view(4, 6).t()]),
+                            (decay, lambda: rec(x, x, x), [decay.data.view(torch.bfloat16), decay.data[:3], decay.data[:1].expand(6)])):
+        good = t.data
+        for other in others:
+            assert other.data_ptr() == good.data_ptr()
+            t.data = other
+            with pytest.raises(TypeError if other.dtype != torch.float32 else ValueError) as err:
+                call()
+            assert "CUDA" not in str(err.value)
+        t.data = good
+
+
 def test_reference_gradients_against_differences():
     """The 64-bit reference's own gradients, against central differences of its loss."""
     gen = torch.Generator().manual_seed(3)
